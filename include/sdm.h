@@ -377,6 +377,185 @@ sdm_status sdm_decode_step_decay(const sdm_shape* shape, const void* q, const vo
 sdm_status sdm_materialize(const sdm_shape* shape, const void* M, const double* lam, const double* lrun, float* out,
                            void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * The dense linear recurrence beside the sparse memory, and the residual block around both:
+ * a short causal convolution, a selective state space scan that reads its output, and the
+ * norm that joins a layer's output to the residual stream. A layer built from them is
+ *   sdm_short_conv -> sdm_selective_scan -> sdm_output_project -> sdm_block_norm
+ * (the scan's o is what sdm_output_gate and sdm_output_project read). PL §2 "Gated DeltaNet"
+ * (a dense state with a scalar decay per head and token), PL §4 "Baselines" (short
+ * convolutions, dense-state layers).
+ *
+ * Tensors of a wider projection: where a shape below has a token stride ld_*, row b*T + t of
+ * that tensor starts at element (b*T + t)*ld_* of its pointer, so it may be a slice of the
+ * columns of a wider row-major buffer. Token strides of in_dtype tensors are multiples of 8
+ * elements, and slices start at 16-byte aligned addresses. An output may share a buffer with
+ * another tensor of the same token stride (in bytes) if their columns are apart.
+ *
+ * Ragged batches: `lengths` [B] int32 (NULL: every sequence has T tokens) gives each
+ * sequence's number of tokens, clamped to [0, T] on the device. Tokens at and behind the
+ * length are padding: whatever they hold (NaN included) has no effect, their outputs and
+ * their gradients are written as 0, and a sequence's final state is the state after its last
+ * token (its initial state if the length is 0).
+ * --------------------------------------------------------------------------------------- */
+
+typedef enum { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1, SDM_ACT_SIGMOID = 2 } sdm_act;
+
+/* Shape of the short convolution. B >= 1, T >= 0, C >= 1 a multiple of 8 (else
+ * SDM_ERR_UNSUPPORTED), 2 <= K <= 8, act SDM_ACT_NONE or SDM_ACT_SILU; ld_x, ld_y >= C,
+ * multiples of 8; B*T <= 2^30 - 1, C <= 2^20, ld_x, ld_y <= 2^24. */
+typedef struct {
+  int32_t B, T;       /* sequences, tokens per sequence in this call       */
+  int32_t C, K;       /* channels, taps                                    */
+  int32_t in_dtype;   /* sdm_dtype of x, y and the state                   */
+  int32_t act;        /* sdm_act                                           */
+  int64_t ld_x, ld_y; /* token strides of x (and dx) and of y (and dy)     */
+} sdm_conv_shape;
+
+sdm_status sdm_check_conv_shape(const sdm_conv_shape* shape);
+
+/* Causal convolution of every channel with its own K taps:
+ *   y[b,t,c] = act(bias[c] + sum_{j<K} w[c,j] X[b, t-(K-1)+j, c])
+ * where X continues x into the past with the state: X[b, -(K-1)+i] = s_in[b,i] (0 if NULL).
+ * The state after the call is the last K-1 inputs of each sequence, oldest first.
+ *   x, y [B,T,C] in_dtype (token strides ld_x, ld_y); w [C,K] f32; bias [C] f32 or NULL
+ *   s_in, s_out [B,K-1,C] in_dtype, each may be NULL; s_out may be s_in itself, else apart.
+ * float32 arithmetic, one rounding to in_dtype. */
+sdm_status sdm_short_conv(const sdm_conv_shape* shape, const void* x, const float* w, const float* bias,
+                          const int32_t* lengths, const void* s_in, void* s_out, void* y, void* stream);
+
+/* One token of every sequence (T must be 1): sdm_short_conv with the state updated in place,
+ * one kernel launch. */
+sdm_status sdm_short_conv_step(const sdm_conv_shape* shape, const void* x, const float* w, const float* bias,
+                               void* state, void* y, void* stream);
+
+/* Bytes of device memory sdm_short_conv_backward needs as workspace (partial sums of dw and
+ * dbias). 0 if the shape is invalid. */
+size_t sdm_short_conv_backward_workspace_bytes(const sdm_conv_shape* shape);
+
+/* Gradients of L = sum <dy, y> + <ds_out, s_out>:
+ *   dy [B,T,C] f32 (token stride ld_y); ds_out [B,K-1,C] f32 or NULL (zeros)
+ *   dx [B,T,C] f32 out (token stride ld_x); dw [C,K] f32 out; dbias [C] f32 out (NULL iff bias
+ *   is); ds_in [B,K-1,C] f32 out or NULL
+ * The activations are recomputed from x. Sums run in a fixed order: the same inputs give the
+ * same bits. ws: at least sdm_short_conv_backward_workspace_bytes(shape) bytes. */
+sdm_status sdm_short_conv_backward(const sdm_conv_shape* shape, const void* x, const float* w, const float* bias,
+                                   const int32_t* lengths, const void* s_in, const float* dy, const float* ds_out,
+                                   float* dx, float* dw, float* dbias, float* ds_in, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/* Shape of the selective scan. B, H >= 1, T >= 0; G >= 1 divides H (head h reads group
+ * h / (H/G)); d_k and d_v >= 1 multiples of 8 with d_k <= 128 and d_v <= 256 (else
+ * SDM_ERR_UNSUPPORTED); ld_x >= H*d_v, ld_b, ld_c >= G*d_k, multiples of 8; ld_dt >= H;
+ * B*T <= 2^30 - 1, B*H <= 65535, H <= 4096, token strides <= 2^24. */
+typedef struct {
+  int32_t B, T;       /* sequences, tokens per sequence in this call               */
+  int32_t H, G;       /* heads, groups of heads that share B and C                 */
+  int32_t d_k, d_v;   /* state width per channel, channels per head                */
+  int32_t in_dtype;   /* sdm_dtype of x, B and C                                   */
+  int64_t ld_x, ld_b, ld_c, ld_dt; /* token strides of x, B, C, dt and their gradients */
+} sdm_scan_shape;
+
+sdm_status sdm_check_scan_shape(const sdm_scan_shape* shape);
+
+/* Bytes of device memory sdm_selective_scan needs as workspace: the states at the starts of
+ * the token segments that a call with few heads is split into (0 if it is not split, or if the
+ * shape is invalid). */
+size_t sdm_selective_scan_workspace_bytes(const sdm_scan_shape* shape);
+
+/* Selective state space scan. For each sequence and head, tokens in order:
+ *   dtv = softplus(dt[b,t,h] + dt_bias[h]);  a = exp(-exp(A_log[h]) * dtv)
+ *   S = a S + dtv x[b,t,h,:] Bm[b,t,g,:]^T          (S [d_v, d_k], g = h / (H/G))
+ *   o[b,h,t,:] = S Cm[b,t,g,:] + D[h] x[b,t,h,:]
+ *   x [B,T,H*d_v], Bm, Cm [B,T,G*d_k] in_dtype (token strides ld_x, ld_b, ld_c)
+ *   dt [B,T,H] f32 (token stride ld_dt); A_log, dt_bias [H] f32; D [H] f32 or NULL (zeros)
+ *   s_in, s_out [B,H,d_v,d_k] f32: the state before (NULL: zeros) and after the call (NULL: not
+ *   wanted); s_out may be s_in itself, else apart
+ *   o [B,H,T,d_v] f32 out
+ * Computed in blocks of tokens on the matrix cores: every float32 factor enters them as three
+ * bf16 pieces that add up to it exactly, and sums are float32; log-decays are added up in
+ * float64 (and floored at -1000 per token, a decay of 0 in float32). A NaN or an infinity at a
+ * token reaches no earlier token's output.
+ * ws: at least sdm_selective_scan_workspace_bytes(shape) bytes (may be NULL if that is 0),
+ * apart from every other buffer and not shared with a call that may run at the same time. */
+sdm_status sdm_selective_scan(const sdm_scan_shape* shape, const void* x, const void* Bm, const void* Cm,
+                              const float* dt, const float* A_log, const float* dt_bias, const float* D,
+                              const int32_t* lengths, const float* s_in, float* s_out, float* o, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* One token of every sequence (T must be 1): sdm_selective_scan with the state [B,H,d_v,d_k]
+ * updated in place, in one kernel launch that reads and writes it once; no workspace. */
+sdm_status sdm_selective_scan_step(const sdm_scan_shape* shape, const void* x, const void* Bm, const void* Cm,
+                                   const float* dt, const float* A_log, const float* dt_bias, const float* D,
+                                   float* state, float* o, void* stream);
+
+/* Bytes of device memory sdm_selective_scan_backward needs as workspace: the states and their
+ * gradients at every 64th token, per-head sums, and partial gradients of Bm and Cm. 0 if the
+ * shape is invalid. */
+size_t sdm_selective_scan_backward_workspace_bytes(const sdm_scan_shape* shape);
+
+/* Gradients of L = sum <go, o> + <ds_out, s_out>. With U the gradient of the state after
+ * token t (from o_t and everything later), e = -exp(A_log[h]):
+ *   dCm_t = sum over the group's heads of S_t^T go_t;  dx_t = dtv U Bm_t + D go_t
+ *   dBm_t = sum over the group's heads of dtv U^T x_t;  dD = sum_t <go_t, x_t>
+ *   dl = a <U, S_{t-1}>  (gradient of log a);  ddt = (x_t^T U Bm_t + e dl) sigmoid(dt + dt_bias)
+ *   dA_log = sum_t e dtv dl;  ddt_bias = sum_t ddt;  then U goes on to token t-1 as a U
+ *   go [B,H,T,d_v] f32; ds_out [B,H,d_v,d_k] f32 or NULL (zeros)
+ *   dx, dBm, dCm f32 out (token strides ld_x, ld_b, ld_c); ddt [B,T,H] f32 out (token stride
+ *   ld_dt); dA_log, ddt_bias [H] f32 out; dD [H] f32 out (NULL iff D is); ds_in [B,H,d_v,d_k]
+ *   f32 out or NULL
+ * The states are recomputed from the inputs. Sums run in a fixed order: the same inputs give
+ * the same bits. A NaN or an infinity among the inputs may reach every gradient of its
+ * sequence. ws: at least sdm_selective_scan_backward_workspace_bytes(shape) bytes, as above. */
+sdm_status sdm_selective_scan_backward(const sdm_scan_shape* shape, const void* x, const void* Bm, const void* Cm,
+                                       const float* dt, const float* A_log, const float* dt_bias, const float* D,
+                                       const int32_t* lengths, const float* s_in, const float* go,
+                                       const float* ds_out, float* dx, float* dBm, float* dCm, float* ddt,
+                                       float* dA_log, float* ddt_bias, float* dD, float* ds_in, void* ws,
+                                       size_t ws_bytes, void* stream);
+
+/* Shape of the block norm. M >= 0 rows (tokens) of D values, D a multiple of 8 (else
+ * SDM_ERR_UNSUPPORTED) and at most 16384, M <= 2^30 - 1; gate_rows >= 0 (0: no gate) divides M:
+ * gate row i serves rows [i*M/gate_rows, (i+1)*M/gate_rows), so gate_rows 1 is a gate of each
+ * channel, B one of each sequence, M one of each token; 0 <= eps <= 1; scale finite. */
+typedef struct {
+  int64_t M;
+  int32_t D;
+  int32_t y_dtype, r_dtype, x_dtype, gate_dtype; /* sdm_dtype of y, r and r_out, x, gate */
+  int32_t gate_act;                              /* sdm_act of the gate                  */
+  int64_t gate_rows;
+  float eps, scale;
+} sdm_norm_shape;
+
+sdm_status sdm_check_norm_shape(const sdm_norm_shape* shape);
+
+/* The norms after one layer and before the next, with the residual sum between them:
+ *   u = y / sqrt(mean(y^2) + eps) * w_post           (u = y if w_post is NULL)
+ *   r_out = r + scale * act(gate) * u                (act(gate) = 1 without a gate)
+ *   x = r_out / sqrt(mean(r_out^2) + eps) * w_pre    (if x is not NULL)
+ *   y [M,D] y_dtype: the layer's output; r, r_out [M,D] r_dtype: the residual stream before and
+ *   after (r_out may be r itself, else apart); gate [gate_rows,D] gate_dtype (NULL iff gate_rows
+ *   is 0); w_post, w_pre [D] f32; x [M,D] x_dtype out, NULL iff w_pre is.
+ * float32 arithmetic; x is formed from r_out before its rounding to r_dtype. A row of zeros
+ * with eps = 0 normalises to zeros. */
+sdm_status sdm_block_norm(const sdm_norm_shape* shape, const void* y, const void* r, const void* gate,
+                          const float* w_post, const float* w_pre, void* r_out, void* x, void* stream);
+
+/* Bytes of device memory sdm_block_norm_backward needs as workspace (partial column sums). 0
+ * if the shape is invalid. */
+size_t sdm_block_norm_backward_workspace_bytes(const sdm_norm_shape* shape);
+
+/* Gradients of L = sum <dr_out, r_out> + <dx, x>; r is the residual stream before the call.
+ *   dr_out [M,D] f32 or NULL (zeros); dx [M,D] f32, NULL iff w_pre is
+ *   dy, dr [M,D] f32 out; dgate [gate_rows,D] f32 out (NULL iff gate is); dw_post, dw_pre [D]
+ *   f32 out (NULL iff w_post, w_pre are)
+ * dr may be dr_out itself, else every output is apart from everything. The roundings of r_out
+ * and x are passed through. Sums run in a fixed order: the same inputs give the same bits. */
+sdm_status sdm_block_norm_backward(const sdm_norm_shape* shape, const void* y, const void* r, const void* gate,
+                                   const float* w_post, const float* w_pre, const float* dr_out, const float* dx,
+                                   float* dy, float* dr, float* dgate, float* dw_post, float* dw_pre, void* ws,
+                                   size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,10 +21,19 @@ __all__ = [
     "decay_state_init", "workspace_bytes_decay", "recurrent_decay", "forward_decay", "decode_step_decay",
     "materialize", "gates", "output_gate", "head_mix", "output_project", "recurrent_log", "recurrent_backward",
     "backward_workspace_bytes", "address_backward", "workspace_bytes_chunked", "recurrent_chunked",
+    "SDM_ACT_NONE", "SDM_ACT_SILU", "SDM_ACT_SIGMOID", "ConvShape", "ScanShape", "NormShape",
+    "make_conv_shape", "check_conv_shape", "short_conv", "short_conv_step", "short_conv_backward",
+    "short_conv_backward_workspace_bytes", "make_scan_shape", "check_scan_shape", "selective_scan",
+    "selective_scan_workspace_bytes", "selective_scan_step", "selective_scan_backward",
+    "selective_scan_backward_workspace_bytes", "make_norm_shape", "check_norm_shape", "block_norm",
+    "block_norm_backward", "block_norm_backward_workspace_bytes",
 ]
 
 SDM_F32 = 0
 SDM_BF16 = 1
+SDM_ACT_NONE = 0
+SDM_ACT_SILU = 1
+SDM_ACT_SIGMOID = 2
 STATIC_SCRATCH_BYTES = 64 << 20  # SDM_STATIC_SCRATCH_BYTES of the header
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -51,7 +60,33 @@ class Shape(ctypes.Structure):
     ]
 
     def __repr__(self):
-        return "Shape(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+        return type(self).__name__ + "(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class ConvShape(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("C", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+    ]
+    __repr__ = Shape.__repr__
+
+
+class ScanShape(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("G", ctypes.c_int32),
+        ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32), ("in_dtype", ctypes.c_int32),
+        ("ld_x", ctypes.c_int64), ("ld_b", ctypes.c_int64), ("ld_c", ctypes.c_int64), ("ld_dt", ctypes.c_int64),
+    ]
+    __repr__ = Shape.__repr__
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("D", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("r_dtype", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32), ("gate_act", ctypes.c_int32),
+        ("gate_rows", ctypes.c_int64), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+    ]
+    __repr__ = Shape.__repr__
 
 
 _lib = None
@@ -88,6 +123,21 @@ _SIGS = {
     "sdm_recurrent_chunked": (ctypes.c_int, [_SP] + [_P] * 10 + [ctypes.c_size_t, _P]),
     "sdm_address_backward": (ctypes.c_int, [_SP, _P, _P, ctypes.c_int32, _P, _P, _P, _P, _P, _P]),
     "sdm_recurrent_backward": (ctypes.c_int, [_SP] + [_P] * 17 + [ctypes.c_size_t, _P]),
+    "sdm_check_conv_shape": (ctypes.c_int, [_P]),
+    "sdm_short_conv": (ctypes.c_int, [_P] * 9),
+    "sdm_short_conv_step": (ctypes.c_int, [_P] * 7),
+    "sdm_short_conv_backward_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "sdm_short_conv_backward": (ctypes.c_int, [_P] * 13 + [ctypes.c_size_t, _P]),
+    "sdm_check_scan_shape": (ctypes.c_int, [_P]),
+    "sdm_selective_scan_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "sdm_selective_scan": (ctypes.c_int, [_P] * 13 + [ctypes.c_size_t, _P]),
+    "sdm_selective_scan_step": (ctypes.c_int, [_P] * 11),
+    "sdm_selective_scan_backward_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "sdm_selective_scan_backward": (ctypes.c_int, [_P] * 21 + [ctypes.c_size_t, _P]),
+    "sdm_check_norm_shape": (ctypes.c_int, [_P]),
+    "sdm_block_norm": (ctypes.c_int, [_P] * 9),
+    "sdm_block_norm_backward_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "sdm_block_norm_backward": (ctypes.c_int, [_P] * 14 + [ctypes.c_size_t, _P]),
 }
 
 
@@ -120,12 +170,20 @@ def abi_version() -> int:
 
 
 def make_shape(B, H, T, N, d_k, d_v, kappa, W, R, in_dtype=SDM_BF16, mem_dtype=SDM_BF16) -> Shape:
-    def dt(x):
-        if isinstance(x, str):
-            return {"f32": SDM_F32, "bf16": SDM_BF16}[x]
-        return int(x)
-    return Shape(int(B), int(H), int(T), int(N), int(d_k), int(d_v), int(kappa), int(W), int(R), dt(in_dtype),
-                 dt(mem_dtype))
+    return Shape(int(B), int(H), int(T), int(N), int(d_k), int(d_v), int(kappa), int(W), int(R), _dt(in_dtype),
+                 _dt(mem_dtype))
+
+
+def _dt(x) -> int:
+    if isinstance(x, str):
+        return {"f32": SDM_F32, "bf16": SDM_BF16}[x]
+    return int(x)
+
+
+def _act(x) -> int:
+    if isinstance(x, str):
+        return {"none": SDM_ACT_NONE, "silu": SDM_ACT_SILU, "sigmoid": SDM_ACT_SIGMOID}[x]
+    return int(x)
 
 
 def _ptr(t) -> Optional[int]:
@@ -300,3 +358,213 @@ def recurrent_chunked(shape: Shape, widx, wgt, ridx, rgt, v, alpha, beta, M, o, 
     _check(lib().sdm_recurrent_chunked(ctypes.byref(shape), _ptr(widx), _ptr(wgt), _ptr(ridx), _ptr(rgt), _ptr(v),
                                        _ptr(alpha), _ptr(beta), _ptr(M), _ptr(o), _ptr(ws),
                                        ws.numel() * ws.element_size(), _stream(stream)), "sdm_recurrent_chunked")
+
+
+# ----------------------------------------------------------------------------- convolution, scan, norm
+class _Args:
+    """Pointers of one call's tensors: each checked for dtype, shape and strides, and for lying on the
+    one GPU of the call, before the library sees an address."""
+
+    def __init__(self, where: str):
+        self.where, self.device = where, None
+
+    def _take(self, name, t, dtype, optional):
+        import torch
+        if t is None:
+            if not optional:
+                raise ValueError(f"{self.where}: {name} is missing")
+            return None
+        want = (torch.float32, torch.bfloat16)[dtype] if isinstance(dtype, int) else dtype
+        if t.dtype != want:
+            raise ValueError(f"{self.where}: {name} is {t.dtype}, not {want}")
+        if not t.is_cuda:
+            raise ValueError(f"{self.where}: {name} is not on a GPU")
+        if self.device is None:
+            self.device = t.device
+        elif t.device != self.device:
+            raise ValueError(f"{self.where}: {name} is on {t.device}, another tensor on {self.device}")
+        return t.data_ptr()
+
+    def flat(self, name, t, dtype, *shape, optional=False):
+        """A contiguous tensor of `shape`."""
+        p = self._take(name, t, dtype, optional)
+        if t is not None and (t.shape != shape or not t.is_contiguous()):
+            raise ValueError(f"{self.where}: {name} has shape {tuple(t.shape)} and strides {t.stride()}, not a "
+                             f"contiguous {shape}")
+        return p
+
+    def rows(self, name, t, dtype, B, T, width, ld):
+        """[B, T, width], or [B, T, ...] with the last dimensions flattened to `width`: rows `ld` apart."""
+        p = self._take(name, t, dtype, False)
+        ok = t.dim() >= 3 and t.shape[0] == B and t.shape[1] == T
+        inner = 1
+        if ok:
+            for d in range(t.dim() - 1, 1, -1):
+                ok = ok and (t.shape[d] == 1 or t.stride(d) == inner)
+                inner *= t.shape[d]
+            ok = ok and inner == width and (T <= 1 or t.stride(1) == ld) and (B == 1 or T == 0 or
+                                                                              t.stride(0) == T * ld)
+        if not ok:
+            raise ValueError(f"{self.where}: {name} has shape {tuple(t.shape)} and strides {t.stride()}, not rows of "
+                             f"{width} values with token stride {ld} for B={B}, T={T}")
+        return p
+
+    def workspace(self, ws):
+        """(pointer, bytes) of the workspace; its size is checked by the library."""
+        if ws is None:
+            return None, 0
+        p = self._take("ws", ws, ws.dtype, False)
+        if not ws.is_contiguous():
+            raise ValueError(f"{self.where}: ws is not contiguous")
+        return p, ws.numel() * ws.element_size()
+
+    def call(self, shape, stream, *args):
+        """Runs the entry point on `stream`, or on the current stream of the tensors' GPU."""
+        import torch
+        f = getattr(lib(), self.where)
+        dev = self.device
+        if dev is None or dev.index == torch.cuda.current_device():
+            _check(f(ctypes.byref(shape), *args, _stream(stream)), self.where)
+            return
+        with torch.cuda.device(dev):
+            _check(f(ctypes.byref(shape), *args, _stream(stream)), self.where)
+
+
+def _i32():
+    import torch
+    return torch.int32
+
+
+def make_conv_shape(B, T, C, K, in_dtype=SDM_BF16, act=SDM_ACT_SILU, ld_x=None, ld_y=None) -> ConvShape:
+    return ConvShape(int(B), int(T), int(C), int(K), _dt(in_dtype), _act(act), int(C if ld_x is None else ld_x),
+                     int(C if ld_y is None else ld_y))
+
+
+def check_conv_shape(shape: ConvShape) -> int:
+    return lib().sdm_check_conv_shape(ctypes.byref(shape))
+
+
+def short_conv(shape: ConvShape, x, w, y, bias=None, lengths=None, s_in=None, s_out=None, stream=None):
+    s, a = shape, _Args("sdm_short_conv")
+    a.call(s, stream, a.rows("x", x, s.in_dtype, s.B, s.T, s.C, s.ld_x), a.flat("w", w, SDM_F32, s.C, s.K),
+           a.flat("bias", bias, SDM_F32, s.C, optional=True), a.flat("lengths", lengths, _i32(), s.B, optional=True),
+           a.flat("s_in", s_in, s.in_dtype, s.B, s.K - 1, s.C, optional=True),
+           a.flat("s_out", s_out, s.in_dtype, s.B, s.K - 1, s.C, optional=True),
+           a.rows("y", y, s.in_dtype, s.B, s.T, s.C, s.ld_y))
+
+
+def short_conv_step(shape: ConvShape, x, w, state, y, bias=None, stream=None):
+    s, a = shape, _Args("sdm_short_conv_step")
+    a.call(s, stream, a.rows("x", x, s.in_dtype, s.B, s.T, s.C, s.ld_x), a.flat("w", w, SDM_F32, s.C, s.K),
+           a.flat("bias", bias, SDM_F32, s.C, optional=True),
+           a.flat("state", state, s.in_dtype, s.B, s.K - 1, s.C), a.rows("y", y, s.in_dtype, s.B, s.T, s.C, s.ld_y))
+
+
+def short_conv_backward_workspace_bytes(shape: ConvShape) -> int:
+    return lib().sdm_short_conv_backward_workspace_bytes(ctypes.byref(shape))
+
+
+def short_conv_backward(shape: ConvShape, x, w, dy, dx, dw, ws, bias=None, dbias=None, lengths=None, s_in=None,
+                        ds_out=None, ds_in=None, stream=None):
+    s, a = shape, _Args("sdm_short_conv_backward")
+    a.call(s, stream, a.rows("x", x, s.in_dtype, s.B, s.T, s.C, s.ld_x), a.flat("w", w, SDM_F32, s.C, s.K),
+           a.flat("bias", bias, SDM_F32, s.C, optional=True), a.flat("lengths", lengths, _i32(), s.B, optional=True),
+           a.flat("s_in", s_in, s.in_dtype, s.B, s.K - 1, s.C, optional=True),
+           a.rows("dy", dy, SDM_F32, s.B, s.T, s.C, s.ld_y),
+           a.flat("ds_out", ds_out, SDM_F32, s.B, s.K - 1, s.C, optional=True),
+           a.rows("dx", dx, SDM_F32, s.B, s.T, s.C, s.ld_x), a.flat("dw", dw, SDM_F32, s.C, s.K),
+           a.flat("dbias", dbias, SDM_F32, s.C, optional=True),
+           a.flat("ds_in", ds_in, SDM_F32, s.B, s.K - 1, s.C, optional=True), *a.workspace(ws))
+
+
+def make_scan_shape(B, T, H, G, d_k, d_v, in_dtype=SDM_BF16, ld_x=None, ld_b=None, ld_c=None, ld_dt=None) -> ScanShape:
+    return ScanShape(int(B), int(T), int(H), int(G), int(d_k), int(d_v), _dt(in_dtype),
+                     int(H * d_v if ld_x is None else ld_x), int(G * d_k if ld_b is None else ld_b),
+                     int(G * d_k if ld_c is None else ld_c), int(H if ld_dt is None else ld_dt))
+
+
+def check_scan_shape(shape: ScanShape) -> int:
+    return lib().sdm_check_scan_shape(ctypes.byref(shape))
+
+
+def _scan_inputs(a: _Args, s: ScanShape, x, Bm, Cm, dt, A_log, dt_bias, D):
+    return (a.rows("x", x, s.in_dtype, s.B, s.T, s.H * s.d_v, s.ld_x),
+            a.rows("Bm", Bm, s.in_dtype, s.B, s.T, s.G * s.d_k, s.ld_b),
+            a.rows("Cm", Cm, s.in_dtype, s.B, s.T, s.G * s.d_k, s.ld_c), a.rows("dt", dt, SDM_F32, s.B, s.T, s.H, s.ld_dt),
+            a.flat("A_log", A_log, SDM_F32, s.H), a.flat("dt_bias", dt_bias, SDM_F32, s.H),
+            a.flat("D", D, SDM_F32, s.H, optional=True))
+
+
+def selective_scan_workspace_bytes(shape: ScanShape) -> int:
+    return lib().sdm_selective_scan_workspace_bytes(ctypes.byref(shape))
+
+
+def selective_scan(shape: ScanShape, x, Bm, Cm, dt, A_log, dt_bias, o, ws=None, D=None, lengths=None, s_in=None,
+                   s_out=None, stream=None):
+    s, a = shape, _Args("sdm_selective_scan")
+    state = (s.B, s.H, s.d_v, s.d_k)
+    a.call(s, stream, *_scan_inputs(a, s, x, Bm, Cm, dt, A_log, dt_bias, D),
+           a.flat("lengths", lengths, _i32(), s.B, optional=True),
+           a.flat("s_in", s_in, SDM_F32, *state, optional=True), a.flat("s_out", s_out, SDM_F32, *state, optional=True),
+           a.flat("o", o, SDM_F32, s.B, s.H, s.T, s.d_v), *a.workspace(ws))
+
+
+def selective_scan_step(shape: ScanShape, x, Bm, Cm, dt, A_log, dt_bias, state, o, D=None, stream=None):
+    s, a = shape, _Args("sdm_selective_scan_step")
+    a.call(s, stream, *_scan_inputs(a, s, x, Bm, Cm, dt, A_log, dt_bias, D),
+           a.flat("state", state, SDM_F32, s.B, s.H, s.d_v, s.d_k), a.flat("o", o, SDM_F32, s.B, s.H, s.T, s.d_v))
+
+
+def selective_scan_backward_workspace_bytes(shape: ScanShape) -> int:
+    return lib().sdm_selective_scan_backward_workspace_bytes(ctypes.byref(shape))
+
+
+def selective_scan_backward(shape: ScanShape, x, Bm, Cm, dt, A_log, dt_bias, go, dx, dBm, dCm, ddt, dA_log, ddt_bias,
+                            ws, D=None, dD=None, lengths=None, s_in=None, ds_out=None, ds_in=None, stream=None):
+    s, a = shape, _Args("sdm_selective_scan_backward")
+    state = (s.B, s.H, s.d_v, s.d_k)
+    a.call(s, stream, *_scan_inputs(a, s, x, Bm, Cm, dt, A_log, dt_bias, D),
+           a.flat("lengths", lengths, _i32(), s.B, optional=True),
+           a.flat("s_in", s_in, SDM_F32, *state, optional=True), a.flat("go", go, SDM_F32, s.B, s.H, s.T, s.d_v),
+           a.flat("ds_out", ds_out, SDM_F32, *state, optional=True),
+           a.rows("dx", dx, SDM_F32, s.B, s.T, s.H * s.d_v, s.ld_x),
+           a.rows("dBm", dBm, SDM_F32, s.B, s.T, s.G * s.d_k, s.ld_b),
+           a.rows("dCm", dCm, SDM_F32, s.B, s.T, s.G * s.d_k, s.ld_c),
+           a.rows("ddt", ddt, SDM_F32, s.B, s.T, s.H, s.ld_dt), a.flat("dA_log", dA_log, SDM_F32, s.H),
+           a.flat("ddt_bias", ddt_bias, SDM_F32, s.H), a.flat("dD", dD, SDM_F32, s.H, optional=True),
+           a.flat("ds_in", ds_in, SDM_F32, *state, optional=True), *a.workspace(ws))
+
+
+def make_norm_shape(M, D, y_dtype=SDM_F32, r_dtype=SDM_F32, x_dtype=SDM_BF16, gate_dtype=SDM_F32, gate_rows=0,
+                    gate_act=SDM_ACT_NONE, eps=1e-5, scale=1.0) -> NormShape:
+    return NormShape(int(M), int(D), _dt(y_dtype), _dt(r_dtype), _dt(x_dtype), _dt(gate_dtype), _act(gate_act),
+                     int(gate_rows), float(eps), float(scale))
+
+
+def check_norm_shape(shape: NormShape) -> int:
+    return lib().sdm_check_norm_shape(ctypes.byref(shape))
+
+
+def block_norm(shape: NormShape, y, r, r_out, gate=None, w_post=None, w_pre=None, x=None, stream=None):
+    s, a = shape, _Args("sdm_block_norm")
+    a.call(s, stream, a.flat("y", y, s.y_dtype, s.M, s.D), a.flat("r", r, s.r_dtype, s.M, s.D),
+           a.flat("gate", gate, s.gate_dtype, s.gate_rows, s.D, optional=True),
+           a.flat("w_post", w_post, SDM_F32, s.D, optional=True), a.flat("w_pre", w_pre, SDM_F32, s.D, optional=True),
+           a.flat("r_out", r_out, s.r_dtype, s.M, s.D), a.flat("x", x, s.x_dtype, s.M, s.D, optional=True))
+
+
+def block_norm_backward_workspace_bytes(shape: NormShape) -> int:
+    return lib().sdm_block_norm_backward_workspace_bytes(ctypes.byref(shape))
+
+
+def block_norm_backward(shape: NormShape, y, r, dy, dr, ws, gate=None, w_post=None, w_pre=None, dr_out=None, dx=None,
+                        dgate=None, dw_post=None, dw_pre=None, stream=None):
+    s, a = shape, _Args("sdm_block_norm_backward")
+    a.call(s, stream, a.flat("y", y, s.y_dtype, s.M, s.D), a.flat("r", r, s.r_dtype, s.M, s.D),
+           a.flat("gate", gate, s.gate_dtype, s.gate_rows, s.D, optional=True),
+           a.flat("w_post", w_post, SDM_F32, s.D, optional=True), a.flat("w_pre", w_pre, SDM_F32, s.D, optional=True),
+           a.flat("dr_out", dr_out, SDM_F32, s.M, s.D, optional=True), a.flat("dx", dx, SDM_F32, s.M, s.D, optional=True),
+           a.flat("dy", dy, SDM_F32, s.M, s.D), a.flat("dr", dr, SDM_F32, s.M, s.D),
+           a.flat("dgate", dgate, SDM_F32, s.gate_rows, s.D, optional=True),
+           a.flat("dw_post", dw_post, SDM_F32, s.D, optional=True), a.flat("dw_pre", dw_pre, SDM_F32, s.D, optional=True),
+           *a.workspace(ws))

@@ -19,10 +19,7 @@ namespace {
 
 constexpr int64_t kMaxN = 262144;  // s <= 512: one half's scores of 32 tokens fit in LDS
 constexpr int kMaxSel = 64;
-constexpr size_t kAlign = 256;
 constexpr size_t kMaxLds = 160 * 1024;
-
-inline size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
 
 // sdm_forward runs the recurrence in its chunkwise two-phase form instead of the pipeline
 // where the two agree up to float32 summation order and the chunkwise form was measured
@@ -34,19 +31,10 @@ bool forward_uses_chunkwise(const sdm_shape& S, bool decay) {
   return !decay && S.mem_dtype == SDM_F32 && (int64_t)S.B * S.H >= 32 && chunked_supported(S);
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 bool mul_ok(size_t a, size_t b, size_t* out) {
   if (a != 0 && b > SIZE_MAX / a) return false;
   *out = a * b;
   return true;
-}
-
-// [p, p+n) and [q, q+m) overlap?
-bool overlaps(const void* p, size_t n, const void* q, size_t m) {
-  if (!p || !q || n == 0 || m == 0) return false;
-  uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  return a < b + m && b < a + n;
 }
 
 sdm_status check_shape(const sdm_shape* S, bool allow_t0) {
@@ -82,8 +70,6 @@ sdm_status check_shape(const sdm_shape* S, bool allow_t0) {
 size_t tensor_bytes(const sdm_shape& S, int64_t last, size_t esize) {
   return (size_t)S.B * S.H * (size_t)S.T * (size_t)last * esize;
 }
-
-sdm_status hip_status(hipError_t e) { return e == hipSuccess ? SDM_OK : SDM_ERR_HIP; }
 
 // Validation of the whole-table decay state against the table, outputs and workspace.
 sdm_status check_decay(const sdm_shape* S, const double* lam, const double* lrun, const void* M, size_t mb,

@@ -84,4 +84,34 @@ __device__ __forceinline__ int mbcnt(uint64_t m) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
 }
 
+// ------------------------------------------------------------------ rows of 8 values
+// 8 consecutive values of a bf16 or float32 row (16-byte aligned) as float32, and back.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* base, long long at, float (&v)[8]) {
+  if (BF16) {
+    const uint4 q = *(const uint4*)((const uint16_t*)base + at);
+    v[0] = bf16lo(q.x); v[1] = bf16hi(q.x); v[2] = bf16lo(q.y); v[3] = bf16hi(q.y);
+    v[4] = bf16lo(q.z); v[5] = bf16hi(q.z); v[6] = bf16lo(q.w); v[7] = bf16hi(q.w);
+  } else {
+    const float4 a = *(const float4*)((const float*)base + at), b = *(const float4*)((const float*)base + at + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void store8(void* base, long long at, const float (&v)[8]) {
+  if (BF16) {
+    *(uint4*)((uint16_t*)base + at) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                 pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  } else {
+    *(float4*)((float*)base + at) = make_float4(v[0], v[1], v[2], v[3]);
+    *(float4*)((float*)base + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// Tokens of sequence b: its length clamped to [0, T], T where no lengths are given.
+__device__ __forceinline__ int sequence_length(const int32_t* lengths, int b, int T) {
+  return lengths ? min(max(lengths[b], 0), T) : T;
+}
+
 }  // namespace sdm

@@ -98,4 +98,75 @@ hipError_t launch_output_project(const sdm_shape& S, const float* o, const void*
 hipError_t launch_materialize(const sdm_shape& S, const void* M, const double* lam, const double* lrun, float* out,
                               hipStream_t stream);
 
+// Argument checks shared by the C ABI files.
+inline size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
+inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+// [p, p+n) and [q, q+m) overlap?
+inline bool overlaps(const void* p, size_t n, const void* q, size_t m) {
+  if (!p || !q || n == 0 || m == 0) return false;
+  uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return a < b + m && b < a + n;
+}
+inline sdm_status hip_status(hipError_t e) { return e == hipSuccess ? SDM_OK : SDM_ERR_HIP; }
+
+// short convolution
+struct ConvArgs {
+  int B, T, C, K;
+  long long ld_x, ld_y;
+  bool bf16, silu;
+  const void* x;
+  const float* w;
+  const float* bias;
+  const int32_t* lengths;
+  const void* s_in;
+  void* s_out;
+  void* y;
+  const float* dy;
+  const float* ds_out;
+  float *dx, *dw, *dbias, *ds_in;
+  float* part;  // backward: partial sums [blocks][C][K+1]
+};
+hipError_t launch_conv(const ConvArgs& A, hipStream_t stream);
+hipError_t launch_conv_backward(const ConvArgs& A, hipStream_t stream);
+size_t conv_backward_workspace_bytes(int B, int T, int C, int K);
+
+// selective scan
+struct ScanArgs {
+  int B, T, H, G, N, P;  // N = d_k, P = d_v
+  long long ld_x, ld_b, ld_c, ld_dt;
+  bool bf16;
+  const void *x, *Bm, *Cm;
+  const float *dt, *A_log, *dt_bias, *D;
+  const int32_t* lengths;
+  const float* s_in;
+  float* s_out;
+  float* o;
+  const float *go, *ds_out;
+  float *dx, *dBm, *dCm, *ddt, *dA_log, *ddt_bias, *dD, *ds_in;
+  void* ws;
+};
+size_t scan_workspace_bytes(const sdm_scan_shape& S);
+size_t scan_backward_workspace_bytes(const sdm_scan_shape& S);
+hipError_t launch_scan(const sdm_scan_shape& S, const ScanArgs& A, hipStream_t stream);
+hipError_t launch_scan_step(const ScanArgs& A, hipStream_t stream);
+hipError_t launch_scan_backward(const sdm_scan_shape& S, const ScanArgs& A, hipStream_t stream);
+
+// block norm
+struct NormArgs {
+  long long M, gate_rows;
+  int D;
+  bool y_bf16, r_bf16, x_bf16, g_bf16;
+  int act;
+  float eps, scale;
+  const void *y, *r, *gate;
+  const float *w_post, *w_pre;
+  void *r_out, *x;
+  const float *dr_out, *dx;
+  float *dy, *dr, *dgate, *dw_post, *dw_pre;
+  float* part;  // backward: partial column sums
+};
+hipError_t launch_norm(const NormArgs& A, hipStream_t stream);
+hipError_t launch_norm_backward(const NormArgs& A, hipStream_t stream);
+size_t norm_backward_workspace_bytes(const sdm_norm_shape& S);
+
 }  // namespace sdm

@@ -3,6 +3,12 @@
 //
 //   dtv = softplus(dt + dt_bias), a = exp(-exp(A_log) dtv)
 //   S_t = a_t S_{t-1} + dtv_t x_t B_t^T,   o_t = S_t C_t + D x_t
+//
+// Prompts run in blocks of Q tokens. With l the log-decay summed from the block's start, S the state
+// before the block and M_ij = (C_i . B_j) exp(l_i - l_j) dtv_j for j <= i:
+//   o_i = exp(l_i) S C_i + sum_j M_ij x_j + D x_i
+//   S'  = exp(l_end) S + sum_j (exp(l_end - l_j) dtv_j x_j) B_j^T
+// all of them matrix products. l is summed in float64, so that the differences keep their digits.
 
 #include "sdm_device.hpp"
 #include "sdm_internal.hpp"
@@ -12,56 +18,401 @@ namespace sdm {
 
 namespace {
 
-// One wave per (sequence, head, channel): its row of the state in registers, token after token.
+constexpr int kPB = 64;  // channels per workgroup: 16 for each of its 4 waves
+
+// Tokens per block: the tiles of three pieces of float32 inputs fill LDS at half the bf16 block
 template <bool BF16>
-__global__ void __launch_bounds__(256) scan_seq_kernel(ScanArgs A) {
-  const long long u = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (u >= (long long)A.B * A.H * A.P) return;
-  const int lane = threadIdx.x & 63;
-  const int p = (int)(u % A.P), h = (int)(u / A.P % A.H), b = (int)(u / A.P / A.H);
-  const int g = h / (A.H / A.G);
+constexpr int block_tokens() { return BF16 ? 64 : 32; }
+
+struct ScanPlan {
+  int pblocks;   // channel blocks per head
+  int blocks;    // token blocks
+  int segments;  // token segments
+};
+
+struct ScanWs {
+  float* first;   // [segments][B*H][P][N]: states before the segments
+  double* decay;  // [segments][B*H]: log2 of the segments' decay
+};
+
+// LDS of one workgroup: tiles of B, C, x (NP planes each) and M (3 planes). Row strides keep the 8-byte
+// reads along rows and the transposing reads over 16 rows on different banks.
+template <bool BF16, int NK>
+struct Tiles {
+  static constexpr int Q = block_tokens<BF16>(), NP = BF16 ? 1 : 3;
+  static constexpr int LB = NK * 32 + 16, LC = NK * 32 + 8, LX = kPB + 16, LM = Q + 8;
+  static constexpr int nB = Q * LB, nC = Q * LC, nX = Q * LX, nM = Q * LM;
+  static constexpr int bytes = (NP * (nB + nC + nX) + 3 * nM) * 2;
+};
+
+// One workgroup walks the blocks of a segment of a (sequence, head, 64 channels) unit with the state in
+// the accumulators of its matrix products: wave w holds channels 16 w .. 16 w + 15, all d_k.
+// STATES: only the state at the segment's end is wanted (of all segments but the last).
+template <bool BF16, int NK, bool STATES>
+__global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, ScanWs W) {
+  using TL = Tiles<BF16, NK>;
+  constexpr int Q = TL::Q, NP = TL::NP, NT = 2 * NK, QT = Q / 16;
+  constexpr int LB = TL::LB, LC = TL::LC, LX = TL::LX, LM = TL::LM, nB = TL::nB, nC = TL::nC, nX = TL::nX, nM = TL::nM;
+  extern __shared__ __align__(16) uint16_t lds[];
+  __shared__ double l_[Q];
+  __shared__ float dtv_[Q], left_[Q];
+  __shared__ int bad_[2];  // does x of the block hold an infinity or a NaN, by the block's parity
+  uint16_t *Bs = lds, *Cs = Bs + NP * nB, *Xs = Cs + NP * nC, *Ms = Xs + NP * nX;
+
+  // unit: the heads of a group side by side on one XCD (workgroups go to the 8 XCDs in turn), so that its
+  // L2 holds the B and C they share
+  const int hpg = A.H / A.G;
+  const int fast = A.B * A.G * (STATES ? L.segments - 1 : L.segments);
+  const int f = blockIdx.x % fast, s = blockIdx.x / fast;
+  const int seg = f / (A.B * A.G), bg = f % (A.B * A.G), b = bg / A.G, g = bg % A.G;
+  const int h = g * hpg + s % hpg, pb = s / hpg;
+  const long long bh = (long long)b * A.H + h;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, lg = lane >> 4, lr = lane & 15;
   const int n = sequence_length(A.lengths, b, A.T);
+  const int N = A.N, P = A.P, p0 = pb * kPB;
+  const int c0 = (int)((long long)L.blocks * seg / L.segments), c1 = (int)((long long)L.blocks * (seg + 1) / L.segments);
   const float rate = -expf(A.A_log[h]), bias = A.dt_bias[h], D = A.D ? A.D[h] : 0.f;
-  float s[2] = {0.f, 0.f};
+
+  // 16-byte pieces of a block's tiles: piece i of this thread lies in row (tid + 256 i) / pieces-per-row
+  constexpr int E = BF16 ? 8 : 4;                              // values per piece
+  constexpr int XR = kPB / E, KR = NK * 32 / E;                // pieces per row
+  constexpr int XN = Q * XR / 256, KN = (Q * KR + 255) / 256;  // pieces per thread
+  constexpr int NX = XN > 0 ? XN : 1;
+  uint4 rx[NX], rb[KN], rc[KN];
+  float rdt = 0.f;
+  const size_t esize = BF16 ? 2 : 4;
+  auto fetch = [&](int c) {
+    const int t0 = c * Q, here = min(max(n - t0, 0), Q);
+    const long long row0 = (long long)b * A.T + t0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (A.s_in && lane + 64 * i < A.N) s[i] = A.s_in[u * A.N + lane + 64 * i];
-  for (int t = 0; t < A.T; ++t) {
-    float o = 0.f;
-    if (t < n) {
-      const long long row = (long long)b * A.T + t;
-      const float dtv = softplus(A.dt[row * A.ld_dt + h] + bias);
-      const float a = expf(fmaxf(rate * dtv, -kMaxDecay));
-      const float x = scan_val<BF16>(A.x, row * A.ld_x + h * A.P + p);
+    for (int i = 0; i < NX; ++i) {
+      const int q = tid + 256 * i, j = q / XR, k = (q % XR) * E;
+      rx[i] = j < here && p0 + k < P
+                  ? *(const uint4*)((const char*)A.x + ((row0 + j) * A.ld_x + h * P + p0 + k) * esize)
+                  : make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int k = lane + 64 * i;
-        if (k < A.N) {
-          s[i] = fmaf(a, s[i], dtv * x * scan_val<BF16>(A.Bm, row * A.ld_b + g * A.N + k));
-          o = fmaf(s[i], scan_val<BF16>(A.Cm, row * A.ld_c + g * A.N + k), o);
+    for (int i = 0; i < KN; ++i) {
+      const int q = tid + 256 * i, j = q / KR, k = (q % KR) * E;
+      const bool in = j < here && k < N;
+      rb[i] = in ? *(const uint4*)((const char*)A.Bm + ((row0 + j) * A.ld_b + g * N + k) * esize)
+                 : make_uint4(0u, 0u, 0u, 0u);
+      if (!STATES)
+        rc[i] = in ? *(const uint4*)((const char*)A.Cm + ((row0 + j) * A.ld_c + g * N + k) * esize)
+                   : make_uint4(0u, 0u, 0u, 0u);
+    }
+    rdt = lane < here ? A.dt[(row0 + lane) * A.ld_dt + h] : 0.f;
+  };
+  // a piece into its tile: as it is, or its four float32 values as three bf16 planes
+  auto put = [&](uint16_t* tile, int plane, int at, const uint4& v) {
+    if (BF16) {
+      *(uint4*)(tile + at) = v;
+    } else {
+      uint32_t a[3], d[3];
+      split_pair(__uint_as_float(v.x), __uint_as_float(v.y), a);
+      split_pair(__uint_as_float(v.z), __uint_as_float(v.w), d);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) *(uint2*)(tile + k * plane + at) = make_uint2(a[k], d[k]);
+    }
+  };
+  // does a piece hold an infinity or a NaN?
+  auto odd = [&](const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    bool r = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r |= BF16 ? (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u
+                : (w[i] & 0x7F800000u) == 0x7F800000u;
+    return r;
+  };
+
+  // state: tile m of 16 d_k x 16 channels; this lane holds channel p0 + 16 wave + lr, d_k 16 m + 4 lg + 0..3
+  const int p = p0 + 16 * wave + lr;
+  const long long srow = (bh * P + p) * N;
+  f32x4_t S[NT];
+  {
+    const float* from = STATES ? nullptr : L.segments > 1 ? W.first + (long long)seg * A.B * A.H * P * N : A.s_in;
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      const int k = 16 * m + 4 * lg;
+      S[m] = from && p < P && k < N ? *(const f32x4_t*)(from + srow + k) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+  double total = 0.0;  // log2 of the decay since the segment's start
+
+  if (!STATES)  // the tiles of M right of the diagonal stay 0
+    for (int i = tid; i < 3 * nM / 8; i += 256) ((uint4*)Ms)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid == 0) bad_[c0 & 1] = 0;
+  fetch(c0);
+  for (int c = c0; c < c1; ++c) {
+    const int t0 = c * Q, here = min(max(n - t0, 0), Q), rows = min(A.T - t0, Q);
+    float* orow = STATES ? nullptr : A.o + (bh * A.T + t0) * P + p0;
+    if (here == 0) {  // behind the sequence's end, like every block after it
+      if (!STATES)
+        for (int i = tid; i < rows * (kPB / 4); i += 256) {
+          const int k = (i % (kPB / 4)) * 4;
+          if (p0 + k < P) *(float4*)(orow + (long long)(i / (kPB / 4)) * P + k) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      continue;
+    }
+    __syncthreads();  // the tiles of the block before are read
+    bool weird = false;
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const int q = tid + 256 * i;
+      if (Q * XR % 256 == 0 || q < Q * XR) put(Xs, nX, q / XR * LX + (q % XR) * E, rx[i]);
+      weird |= odd(rx[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < KN; ++i) {
+      const int q = tid + 256 * i;
+      if (Q * KR % 256 == 0 || q < Q * KR) {
+        put(Bs, nB, q / KR * LB + (q % KR) * E, rb[i]);
+        if (!STATES) put(Cs, nC, q / KR * LC + (q % KR) * E, rc[i]);
+      }
+    }
+    if (!STATES && weird) bad_[c & 1] = 1;
+    // log-decays: one token per lane
+    const float dtv = lane < here ? softplus(rdt + bias) : 0.f;
+    const double l = wave_prefix((double)fmaxf(rate * dtv, -kMaxDecay) * (lane < here ? kLog2e : 0.0));
+    const double end = __shfl(l, 63, 64);
+    if (wave == 0 && lane < Q) {
+      l_[lane] = l;
+      dtv_[lane] = dtv;
+      left_[lane] = exp2_of(end - l) * dtv;
+    }
+    total += end;
+    if (c + 1 < c1) fetch(c + 1);
+    __syncthreads();
+
+    if (!STATES) {
+      if (tid == 0) bad_[(c + 1) & 1] = 0;
+      // M, tiles (it, jt) on and below the diagonal in turn over the waves
+#pragma unroll 1
+      for (int e = wave; e < QT * (QT + 1) / 2; e += 4) {
+        int it = 0, jt = e;
+        while (jt > it) {
+          ++it;
+          jt -= it;
+        }
+        f32x4_t G = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+          mma(G, along<NP>(Bs + 16 * jt * LB + 32 * k, LB, nB, lane), along<NP>(Cs + 16 * it * LC + 32 * k, LC, nC, lane));
+        const int i = 16 * it + lr, j = 16 * jt + 4 * lg;
+        const double li = l_[i];
+        float mv[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mv[u] = j + u <= i ? G[u] * (exp2_of(li - l_[j + u]) * dtv_[j + u]) : 0.f;
+        uint32_t w0[3], w1[3];
+        split_pair(mv[0], mv[1], w0);
+        split_pair(mv[2], mv[3], w1);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *(uint2*)(Ms + k * nM + i * LM + j) = make_uint2(w0[k], w1[k]);
+      }
+      Frag<3> Sf[NK];
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        const float v[8] = {S[2 * k][0], S[2 * k][1], S[2 * k][2], S[2 * k][3],
+                            S[2 * k + 1][0], S[2 * k + 1][1], S[2 * k + 1][2], S[2 * k + 1][3]};
+        Sf[k] = split8(v);
+      }
+      __syncthreads();
+      const bool bad = bad_[c & 1] != 0;
+      Frag<NP> xf[Q / 32];
+#pragma unroll
+      for (int k = 0; k < Q / 32; ++k) xf[k] = across<NP>(Xs + 32 * k * LX + 16 * wave, LX, nX, lane);
+#pragma unroll
+      for (int it = 0; it < QT; ++it) {
+        f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < NK; ++k) mma(y, Sf[k], along<NP>(Cs + 16 * it * LC + 32 * k, LC, nC, lane));
+        const int i = 16 * it + lr;
+        y *= exp2_of(l_[i]);
+        if (!bad) {
+#pragma unroll
+          for (int k = 0; k <= it / 2; ++k) mma(y, xf[k], along<3>(Ms + 16 * it * LM + 32 * k, LM, nM, lane));
+        }
+        float xi[4] = {0.f, 0.f, 0.f, 0.f};  // channels 4 lg .. of this wave, token i
+        for (int k = NP - 1; k >= 0; --k) {
+          const uint2 q = *(const uint2*)(Xs + k * nX + i * LX + 16 * wave + 4 * lg);
+          xi[0] += bf16lo(q.x);
+          xi[1] += bf16hi(q.x);
+          xi[2] += bf16lo(q.y);
+          xi[3] += bf16hi(q.y);
+        }
+        if (bad)  // an infinity or a NaN times the zeros of M would reach earlier tokens: only j <= i
+          for (int j = 0; j <= i; ++j) {
+            const float m = bf16_to_f32(Ms[i * LM + j]) + bf16_to_f32(Ms[nM + i * LM + j]) + bf16_to_f32(Ms[2 * nM + i * LM + j]);
+            for (int k = NP - 1; k >= 0; --k) {
+              const uint2 q = *(const uint2*)(Xs + k * nX + j * LX + 16 * wave + 4 * lg);
+              y[0] = fmaf(m, bf16lo(q.x), y[0]);
+              y[1] = fmaf(m, bf16hi(q.x), y[1]);
+              y[2] = fmaf(m, bf16lo(q.y), y[2]);
+              y[3] = fmaf(m, bf16hi(q.y), y[3]);
+            }
+          }
+        const int k = 16 * wave + 4 * lg;
+        if (i < rows && p0 + k < P) {
+          float4 v = make_float4(fmaf(D, xi[0], y[0]), fmaf(D, xi[1], y[1]), fmaf(D, xi[2], y[2]), fmaf(D, xi[3], y[3]));
+          if (i >= here) v = make_float4(0.f, 0.f, 0.f, 0.f);
+          *(float4*)(orow + (long long)i * P + k) = v;
         }
       }
-      o = wave_sum_f32(o) + D * x;
     }
-    if (lane == 0) A.o[(((long long)b * A.H + h) * A.T + t) * A.P + p] = o;
+    // the state at the block's end
+    const float keep = exp2_of(end);
+#pragma unroll
+    for (int m = 0; m < NT; ++m) S[m] *= keep;
+#pragma unroll
+    for (int k = 0; k < Q / 32; ++k) {
+      float v[8];
+      values_of(across<NP>(Xs + 32 * k * LX + 16 * wave, LX, nX, lane), v);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        v[u] *= left_[32 * k + 4 * lg + u];
+        v[4 + u] *= left_[32 * k + 16 + 4 * lg + u];
+      }
+      const Frag<3> xw = split8(v);
+#pragma unroll
+      for (int m = 0; m < NT; ++m) mma(S[m], across<NP>(Bs + 32 * k * LB + 16 * m, LB, nB, lane), xw);
+    }
+  }
+  float* to = STATES ? W.first + (long long)(seg + 1) * A.B * A.H * P * N : seg + 1 == L.segments ? A.s_out : nullptr;
+  if (to && p < P) {
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      const int k = 16 * m + 4 * lg;
+      if (k < N) *(f32x4_t*)(to + srow + k) = S[m];
+    }
+  }
+  if (STATES && tid == 0 && pb == 0) W.decay[(long long)(seg + 1) * A.B * A.H + bh] = total;
+}
+
+// States before the segments, from the segments' own ends: first[0] is the call's first state, first[s]
+// (which holds what segment s-1 adds) takes up first[s-1] decayed over segment s-1.
+__global__ void __launch_bounds__(256) scan_join_kernel(ScanArgs A, ScanPlan L, ScanWs W) {
+  const long long per = (long long)A.P * A.N / 4, units = (long long)A.B * A.H;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= units * per) return;
+  f32x4_t* v = (f32x4_t*)W.first;
+  f32x4_t s = A.s_in ? ((const f32x4_t*)A.s_in)[i] : f32x4_t{0.f, 0.f, 0.f, 0.f};
+  v[i] = s;
+  for (int k = 1; k < L.segments; ++k) {
+    s = v[k * units * per + i] + s * exp2_of(W.decay[k * units + i / per]);
+    v[k * units * per + i] = s;
+  }
+}
+
+// ------------------------------------------------------------------ single tokens
+// The state goes through the registers once, 16 bytes a lane; LR lanes hold a channel's row.
+template <bool BF16, int LR>
+__global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs A) {
+  constexpr int RW = 64 / LR;  // rows per wave
+  const int blocks = (A.P + 4 * RW - 1) / (4 * RW);
+  const int bh = blockIdx.x / blocks, b = bh / A.H, h = bh % A.H, g = h / (A.H / A.G);
+  const int lane = threadIdx.x & 63, k = (lane % LR) * 4;
+  const int p = (int)(blockIdx.x % blocks) * 4 * RW + (int)(threadIdx.x >> 6) * RW + lane / LR;
+  const bool live = p < A.P && k < A.N;
+  float* row = A.s_out + ((long long)bh * A.P + p) * A.N + k;
+  f32x4_t s = live ? *(const f32x4_t*)row : f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const float dtv = softplus(A.dt[b * A.ld_dt + h] + A.dt_bias[h]);
+  const float a = expf(fmaxf(-expf(A.A_log[h]) * dtv, -kMaxDecay));
+  float o = 0.f, x = 0.f;
+  if (live) {
+    x = scan_val<BF16>(A.x, b * A.ld_x + h * A.P + p);
+    const float w = dtv * x;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      s[u] = fmaf(a, s[u], w * scan_val<BF16>(A.Bm, b * A.ld_b + g * A.N + k + u));
+      o = fmaf(s[u], scan_val<BF16>(A.Cm, b * A.ld_c + g * A.N + k + u), o);
+    }
+    *(f32x4_t*)row = s;
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (A.s_out && lane + 64 * i < A.N) A.s_out[u * A.N + lane + 64 * i] = s[i];
+  for (int m = 1; m < LR; m <<= 1) o = add_xor_f32(o, m);
+  if (live && k == 0) A.o[(long long)bh * A.P + p] = fmaf(A.D ? A.D[h] : 0.f, x, o);
+}
+
+// A call of few units is split into token segments until about two workgroups per compute unit are
+// busy, each of at least four blocks: the pass over x and B that a split costs is then shared by enough.
+ScanPlan plan_of(const sdm_scan_shape& S) {
+  const int Q = S.in_dtype == SDM_BF16 ? block_tokens<true>() : block_tokens<false>();
+  ScanPlan L;
+  L.pblocks = (S.d_v + kPB - 1) / kPB;
+  L.blocks = (S.T + Q - 1) / Q;
+  const long long units = (long long)S.B * S.H * L.pblocks;
+  long long s = 512 / units;
+  if (s > L.blocks / 4) s = L.blocks / 4;
+  L.segments = s < 1 ? 1 : (int)s;
+  return L;
+}
+
+size_t workspace(const sdm_scan_shape& S, const ScanPlan& L, char* base, ScanWs* W) {
+  if (L.segments < 2) return 0;
+  const size_t units = (size_t)S.B * S.H, st = align_up(units * L.segments * S.d_v * S.d_k * 4);
+  W->first = (float*)base;
+  W->decay = (double*)(base + st);
+  return st + align_up(units * L.segments * 8);
+}
+
+template <bool BF16, int NK>
+hipError_t launch_blocks(const ScanArgs& A, const ScanPlan& L, const ScanWs& W, hipStream_t stream) {
+  constexpr int lds = Tiles<BF16, NK>::bytes;
+  const long long units = (long long)A.B * A.H * L.pblocks;
+  hipError_t e;
+  if (L.segments > 1) {
+    hipLaunchKernelGGL((scan_kernel<BF16, NK, true>), dim3((unsigned)(units * (L.segments - 1))), dim3(256), lds, stream,
+                       A, L, W);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const long long quads = (long long)A.B * A.H * A.P * A.N / 4;
+    hipLaunchKernelGGL(scan_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, A, L, W);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((scan_kernel<BF16, NK, false>), dim3((unsigned)(units * L.segments)), dim3(256), lds, stream, A, L, W);
+  return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t launch_step(const ScanArgs& A, hipStream_t stream) {
+  const int quads = A.N / 4;
+#define SDM_STEP(LR)                                                                                      \
+  if (quads <= LR) {                                                                                      \
+    const int rows = 4 * (64 / LR);                                                                       \
+    const long long blocks = (long long)A.B * A.H * ((A.P + rows - 1) / rows);                            \
+    hipLaunchKernelGGL((scan_step_kernel<BF16, LR>), dim3((unsigned)blocks), dim3(256), 0, stream, A); \
+    return hipGetLastError();                                                                             \
+  }
+  SDM_STEP(2) SDM_STEP(4) SDM_STEP(8) SDM_STEP(16) SDM_STEP(32)
+#undef SDM_STEP
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t scan_workspace_bytes(const sdm_scan_shape&) { return 0; }
-
-hipError_t launch_scan(const sdm_scan_shape&, const ScanArgs& A, hipStream_t stream) {
-  const long long units = (long long)A.B * A.H * A.P;
-  const dim3 grid((unsigned)((units + 3) / 4));
-  if (A.bf16) hipLaunchKernelGGL(scan_seq_kernel<true>, grid, dim3(256), 0, stream, A);
-  else hipLaunchKernelGGL(scan_seq_kernel<false>, grid, dim3(256), 0, stream, A);
-  return hipGetLastError();
+size_t scan_workspace_bytes(const sdm_scan_shape& S) {
+  ScanWs W;
+  return workspace(S, plan_of(S), nullptr, &W);
 }
 
-hipError_t launch_scan_step(const ScanArgs& A, hipStream_t stream) { return launch_scan(sdm_scan_shape{}, A, stream); }
+hipError_t launch_scan(const sdm_scan_shape& S, const ScanArgs& A, hipStream_t stream) {
+  const ScanPlan L = plan_of(S);
+  ScanWs W{};
+  workspace(S, L, (char*)A.ws, &W);
+  const int steps = (A.N + 31) / 32;
+  if (A.bf16)
+    return steps == 1   ? launch_blocks<true, 1>(A, L, W, stream)
+           : steps == 2 ? launch_blocks<true, 2>(A, L, W, stream)
+                        : launch_blocks<true, 4>(A, L, W, stream);
+  return steps == 1   ? launch_blocks<false, 1>(A, L, W, stream)
+         : steps == 2 ? launch_blocks<false, 2>(A, L, W, stream)
+                      : launch_blocks<false, 4>(A, L, W, stream);
+}
+
+hipError_t launch_scan_step(const ScanArgs& A, hipStream_t stream) {
+  return A.bf16 ? launch_step<true>(A, stream) : launch_step<false>(A, stream);
+}
 
 }  // namespace sdm

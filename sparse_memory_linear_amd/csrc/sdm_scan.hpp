@@ -1,4 +1,13 @@
-// What the forward and the backward pass of the selective scan share.
+// What the forward and the backward pass of the selective scan share: the factors of the matrix
+// products as bf16 pieces, the reads of operand fragments, the log-decays of a block of tokens.
+//
+// v_mfma_f32_16x16x32_bf16: D[row][col] += sum over k of A[row][k] B[k][col]. Lane l gives A's row (B's
+// column) l % 16 for 8 of the 32 k; the same choice of k for A and B pairs them up whatever the
+// instruction's own order is. Of D the lane holds column l % 16, rows 4 (l / 16) + 0..3.
+//
+// A float32 factor enters as three bf16 pieces that add up to it exactly (each takes the next 8 of the 24
+// bits), a bf16 factor as itself. The product of two factors of n_a and n_b pieces is the sum of the
+// products of the pieces whose ranks add up to at most 2; what is left out is below 2^-23 of it.
 #pragma once
 
 #include "sdm_device.hpp"
@@ -6,8 +15,12 @@
 
 namespace sdm {
 
-constexpr int kScanBlock = 64;        // tokens per block: one per lane of a wave
 constexpr float kMaxDecay = 1000.f;  // floor of a token's log-decay (exp(-1000) is 0 in float32)
+constexpr double kLog2e = 1.4426950408889634074;
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 template <bool BF16>
 __device__ __forceinline__ float scan_val(const void* p, long long at) {
@@ -15,5 +28,111 @@ __device__ __forceinline__ float scan_val(const void* p, long long at) {
 }
 
 __device__ __forceinline__ float softplus(float x) { return x > 20.f ? x : log1pf(expf(x)); }
+
+__device__ __forceinline__ float exp2_of(double x) { return __builtin_amdgcn_exp2f((float)x); }
+
+// High halves of two words as one word (a in the low half)
+__device__ __forceinline__ uint32_t high_halves(float a, float b) {
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ float truncated(float a) { return __uint_as_float(__float_as_uint(a) & 0xFFFF0000u); }
+
+// Two float32 values as three words of two bf16 pieces each
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&w)[3]) {
+  w[0] = high_halves(a, b);
+  a -= truncated(a);
+  b -= truncated(b);
+  w[1] = high_halves(a, b);
+  a -= truncated(a);
+  b -= truncated(b);
+  w[2] = high_halves(a, b);
+}
+
+// One operand fragment: 8 bf16 of each of NP pieces
+template <int NP>
+struct Frag {
+  uint4 v[NP];
+};
+
+// 8 float32 values as a fragment of three pieces
+__device__ __forceinline__ Frag<3> split8(const float (&x)[8]) {
+  Frag<3> f;
+  uint32_t w[4][3];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split_pair(x[2 * i], x[2 * i + 1], w[i]);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) f.v[k] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
+  return f;
+}
+
+// The 8 values of a fragment (the sum of its pieces)
+template <int NP>
+__device__ __forceinline__ void values_of(const Frag<NP>& f, float (&x)[8]) {
+#pragma unroll
+  for (int k = NP - 1; k >= 0; --k) {
+    const uint32_t w[4] = {f.v[k].x, f.v[k].y, f.v[k].z, f.v[k].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float lo = bf16lo(w[i]), hi = bf16hi(w[i]);
+      x[2 * i] = k == NP - 1 ? lo : x[2 * i] + lo;
+      x[2 * i + 1] = k == NP - 1 ? hi : x[2 * i + 1] + hi;
+    }
+  }
+}
+
+template <int NA, int NB>
+__device__ __forceinline__ void mma(f32x4_t& d, const Frag<NA>& a, const Frag<NB>& b) {
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = NB - 1; j >= 0; --j)
+      if (i + j <= 2)
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a.v[i]),
+                                                    __builtin_bit_cast(bf16x8_t, b.v[j]), d, 0, 0, 0);
+}
+
+// Reads of fragments from a tile in LDS, rows `ld` bf16 apart, planes (pieces) `plane` apart. The k of a
+// lane with g = l / 16 are 4g..4g+3 and 16+4g..16+4g+3 of the 32: the order in which a lane holds two
+// stacked 16x16 results, which so become operands without leaving their lanes.
+//
+// along(): row l % 16 of the tile is the operand's row, k runs along it
+template <int NP>
+__device__ __forceinline__ Frag<NP> along(const uint16_t* tile, int ld, int plane, int lane) {
+  Frag<NP> f;
+  const uint16_t* p = tile + (lane & 15) * ld + (lane >> 4) * 4;
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const uint2 a = *(const uint2*)(p + k * plane), b = *(const uint2*)(p + k * plane + 16);
+    f.v[k] = make_uint4(a.x, a.y, b.x, b.y);
+  }
+  return f;
+}
+// across(): column l % 16 of the tile is the operand's row, k runs over the tile's rows. The transposing
+// read hands 16 lanes the columns of four rows of 16 values, whose quarters the lanes address.
+template <int NP>
+__device__ __forceinline__ Frag<NP> across(uint16_t* tile, int ld, int plane, int lane) {
+  typedef __attribute__((address_space(3))) s16x4_t lds_t;
+  Frag<NP> f;
+  uint16_t* p = tile + ((lane >> 4) * 4 + ((lane >> 2) & 3)) * ld + (lane & 3) * 4;
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(p + k * plane)));
+    const uint2 b =
+        __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(p + k * plane + 16 * ld)));
+    f.v[k] = make_uint4(a.x, a.y, b.x, b.y);
+  }
+  return f;
+}
+
+// Inclusive sum over the lanes up to this one
+__device__ __forceinline__ double wave_prefix(double v) {
+  const int lane = lane_id();
+#pragma unroll
+  for (int m = 1; m < kWave; m <<= 1) {
+    const double o = __shfl_up(v, m, kWave);
+    if (lane >= m) v += o;
+  }
+  return v;
+}
 
 }  // namespace sdm

@@ -20,7 +20,7 @@ namespace sdm {
 
 namespace {
 
-constexpr int Q = kScanBlock;
+constexpr int Q = 64;  // tokens per block
 
 struct ScanBwdWs {
   float* S;      // [B,H,nb,P,N] states before the blocks

@@ -447,7 +447,7 @@ sdm_status sdm_short_conv_backward(const sdm_conv_shape* shape, const void* x, c
 /* Shape of the selective scan. B, H >= 1, T >= 0; G >= 1 divides H (head h reads group
  * h / (H/G)); d_k and d_v >= 1 multiples of 8 with d_k <= 128 and d_v <= 256 (else
  * SDM_ERR_UNSUPPORTED); ld_x >= H*d_v, ld_b, ld_c >= G*d_k, multiples of 8; ld_dt >= H;
- * B*T <= 2^30 - 1, B*H <= 65535, H <= 4096, token strides <= 2^24. */
+ * B*T <= 2^30 - 1, B*H <= 65535, H <= 4096, token strides <= 2^22. */
 typedef struct {
   int32_t B, T;       /* sequences, tokens per sequence in this call               */
   int32_t H, G;       /* heads, groups of heads that share B and C                 */

@@ -14,6 +14,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = (int64_t)INT32_MAX / 2;
 constexpr int64_t kMaxStride = (int64_t)1 << 24;
+constexpr int64_t kMaxScanStride = (int64_t)1 << 22;
 
 bool dtype_ok(int dt) { return dt == SDM_F32 || dt == SDM_BF16; }
 
@@ -85,7 +86,8 @@ sdm_status check_scan(const sdm_scan_shape* S) {
       S->ld_dt < S->H)
     return SDM_ERR_INVALID_ARG;
   if (S->ld_x % 8 != 0 || S->ld_b % 8 != 0 || S->ld_c % 8 != 0) return SDM_ERR_UNSUPPORTED;
-  if (S->ld_x > kMaxStride || S->ld_b > kMaxStride || S->ld_c > kMaxStride || S->ld_dt > kMaxStride)
+  // a block of 64 rows is addressed with 32-bit byte offsets
+  if (S->ld_x > kMaxScanStride || S->ld_b > kMaxScanStride || S->ld_c > kMaxScanStride || S->ld_dt > kMaxScanStride)
     return SDM_ERR_UNSUPPORTED;
   if ((int64_t)S->B * S->T > kMaxTokens || (int64_t)S->B * S->H > 65535) return SDM_ERR_UNSUPPORTED;
   return SDM_OK;

@@ -42,7 +42,7 @@ struct Tiles {
   static constexpr int Q = block_tokens<BF16>(), NP = BF16 ? 1 : 3;
   static constexpr int LB = NK * 32 + 16, LC = NK * 32 + 8, LX = kPB + 16, LM = Q + 8;
   static constexpr int nB = Q * LB, nC = Q * LC, nX = Q * LX, nM = Q * LM;
-  static constexpr int bytes = (NP * (nB + nC + nX) + 3 * nM) * 2;
+  static constexpr int bytes = (NP * (nB + nX + nC) + 3 * nM) * 2, states_bytes = NP * (nB + nX) * 2;
 };
 
 // One workgroup walks the blocks of a segment of a (sequence, head, 64 channels) unit with the state in
@@ -54,10 +54,10 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   constexpr int Q = TL::Q, NP = TL::NP, NT = 2 * NK, QT = Q / 16;
   constexpr int LB = TL::LB, LC = TL::LC, LX = TL::LX, LM = TL::LM, nB = TL::nB, nC = TL::nC, nX = TL::nX, nM = TL::nM;
   extern __shared__ __align__(16) uint16_t lds[];
-  __shared__ double l_[Q];
-  __shared__ float dtv_[Q], left_[Q];
+  __shared__ double l_[2][Q];
+  __shared__ __align__(16) float dtv_[2][Q], left_[2][Q];
   __shared__ int bad_[2];  // does x of the block hold an infinity or a NaN, by the block's parity
-  uint16_t *Bs = lds, *Cs = Bs + NP * nB, *Xs = Cs + NP * nC, *Ms = Xs + NP * nX;
+  uint16_t *Bs = lds, *Xs = Bs + NP * nB, *Cs = Xs + NP * nX, *Ms = Cs + NP * nC;
 
   // unit: the heads of a group side by side on one XCD (workgroups go to the 8 XCDs in turn), so that its
   // L2 holds the B and C they share
@@ -67,41 +67,53 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   const int seg = f / (A.B * A.G), bg = f % (A.B * A.G), b = bg / A.G, g = bg % A.G;
   const int h = g * hpg + s % hpg, pb = s / hpg;
   const long long bh = (long long)b * A.H + h;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, lg = lane >> 4, lr = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lg = lane >> 4, lr = lane & 15;
   const int n = sequence_length(A.lengths, b, A.T);
   const int N = A.N, P = A.P, p0 = pb * kPB;
   const int c0 = (int)((long long)L.blocks * seg / L.segments), c1 = (int)((long long)L.blocks * (seg + 1) / L.segments);
   const float rate = -expf(A.A_log[h]), bias = A.dt_bias[h], D = A.D ? A.D[h] : 0.f;
 
-  // 16-byte pieces of a block's tiles: piece i of this thread lies in row (tid + 256 i) / pieces-per-row
-  constexpr int E = BF16 ? 8 : 4;                              // values per piece
-  constexpr int XR = kPB / E, KR = NK * 32 / E;                // pieces per row
-  constexpr int XN = Q * XR / 256, KN = (Q * KR + 255) / 256;  // pieces per thread
-  constexpr int NX = XN > 0 ? XN : 1;
-  uint4 rx[NX], rb[KN], rc[KN];
+  // 16-byte pieces of a block's tiles: piece i of this thread lies in row j + i (256 / pieces-per-row) for
+  // its row j of piece 0, in the same columns; `in` is what the columns allow
+  constexpr int E = BF16 ? 8 : 4, ES = BF16 ? 2 : 4;        // values per piece, bytes per value
+  constexpr int XR = kPB / E, KR = NK * 32 / E;             // pieces per row
+  constexpr int NX = Q * XR / 256, NKV = (Q * KR + 255) / 256;      // pieces per thread
+  constexpr int XS = 256 / XR, KS = 256 / KR;               // rows between pieces
+  const int xj = tid / XR, xk = (tid % XR) * E, kj = tid / KR, kk = (tid % KR) * E;
+  const bool xin = p0 + xk < P, kin = kk < N;
+  const uint32_t xoff = (uint32_t)(xj * A.ld_x + xk) * ES, boff = (uint32_t)(kj * A.ld_b + kk) * ES,
+                 coff = (uint32_t)(kj * A.ld_c + kk) * ES;
+  uint4 rx[NX], rb[NKV], rc[NKV];
   float rdt = 0.f;
-  const size_t esize = BF16 ? 2 : 4;
   auto fetch = [&](int c) {
     const int t0 = c * Q, here = min(max(n - t0, 0), Q);
     const long long row0 = (long long)b * A.T + t0;
+    const char* px = (const char*)A.x + (row0 * A.ld_x + h * P + p0) * ES;
+    const char* pb_ = (const char*)A.Bm + (row0 * A.ld_b + g * N) * ES;
+    const char* pc = (const char*)A.Cm + (row0 * A.ld_c + g * N) * ES;
+    const int xrows = xin ? here : 0, krows = kin ? here : 0;
 #pragma unroll
-    for (int i = 0; i < NX; ++i) {
-      const int q = tid + 256 * i, j = q / XR, k = (q % XR) * E;
-      rx[i] = j < here && p0 + k < P
-                  ? *(const uint4*)((const char*)A.x + ((row0 + j) * A.ld_x + h * P + p0 + k) * esize)
-                  : make_uint4(0u, 0u, 0u, 0u);
-    }
+    for (int i = 0; i < NX; ++i)
+      rx[i] = xj + i * XS < xrows ? *(const uint4*)(px + i * XS * A.ld_x * ES + xoff) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (int i = 0; i < KN; ++i) {
-      const int q = tid + 256 * i, j = q / KR, k = (q % KR) * E;
-      const bool in = j < here && k < N;
-      rb[i] = in ? *(const uint4*)((const char*)A.Bm + ((row0 + j) * A.ld_b + g * N + k) * esize)
-                 : make_uint4(0u, 0u, 0u, 0u);
-      if (!STATES)
-        rc[i] = in ? *(const uint4*)((const char*)A.Cm + ((row0 + j) * A.ld_c + g * N + k) * esize)
-                   : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < NKV; ++i) {
+      const bool in = kj + i * KS < krows;
+      rb[i] = in ? *(const uint4*)(pb_ + i * KS * A.ld_b * ES + boff) : make_uint4(0u, 0u, 0u, 0u);
+      if (!STATES) rc[i] = in ? *(const uint4*)(pc + i * KS * A.ld_c * ES + coff) : make_uint4(0u, 0u, 0u, 0u);
     }
-    rdt = lane < here ? A.dt[(row0 + lane) * A.ld_dt + h] : 0.f;
+    if (wave == 0) rdt = lane < here ? A.dt[(row0 + lane) * A.ld_dt + h] : 0.f;
+  };
+  // log-decays of a block by wave 0, one token per lane, into the arrays of the block's parity
+  auto gates = [&](int c) {
+    const int here = min(max(n - c * Q, 0), Q);
+    const float dtv = lane < here ? softplus(rdt + bias) : 0.f;
+    const double l = wave_prefix((double)fmaxf(rate * dtv, -kMaxDecay) * (lane < here ? kLog2e : 0.0));
+    const double end = last_lane(l);
+    if (lane < Q) {
+      l_[c & 1][lane] = l;
+      dtv_[c & 1][lane] = dtv;
+      left_[c & 1][lane] = exp2_of(end - l) * dtv;
+    }
   };
   // a piece into its tile: as it is, or its four float32 values as three bf16 planes
   auto put = [&](uint16_t* tile, int plane, int at, const uint4& v) {
@@ -126,15 +138,17 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
     return r;
   };
 
-  // state: tile m of 16 d_k x 16 channels; this lane holds channel p0 + 16 wave + lr, d_k 16 m + 4 lg + 0..3
+  // state: tiles of 16 d_k x 16 channels, in pairs over 32 d_k: this lane holds channel p0 + 16 wave + lr,
+  // d_k 32 (m / 2) + 8 lg + 4 (m % 2) + 0..3 of tile m
   const int p = p0 + 16 * wave + lr;
+  auto state_at = [&](int m) { return 32 * (m >> 1) + 8 * lg + 4 * (m & 1); };
   const long long srow = (bh * P + p) * N;
   f32x4_t S[NT];
   {
     const float* from = STATES ? nullptr : L.segments > 1 ? W.first + (long long)seg * A.B * A.H * P * N : A.s_in;
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
-      const int k = 16 * m + 4 * lg;
+      const int k = state_at(m);
       S[m] = from && p < P && k < N ? *(const f32x4_t*)(from + srow + k) : f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
   }
@@ -144,6 +158,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
     for (int i = tid; i < 3 * nM / 8; i += 256) ((uint4*)Ms)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (tid == 0) bad_[c0 & 1] = 0;
   fetch(c0);
+  if (wave == 0) gates(c0);
   for (int c = c0; c < c1; ++c) {
     const int t0 = c * Q, here = min(max(n - t0, 0), Q), rows = min(A.T - t0, Q);
     float* orow = STATES ? nullptr : A.o + (bh * A.T + t0) * P + p0;
@@ -159,56 +174,56 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
     bool weird = false;
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
-      const int q = tid + 256 * i;
-      if (Q * XR % 256 == 0 || q < Q * XR) put(Xs, nX, q / XR * LX + (q % XR) * E, rx[i]);
+      put(Xs, nX, (xj + i * XS) * LX + xk, rx[i]);
       weird |= odd(rx[i]);
     }
 #pragma unroll
-    for (int i = 0; i < KN; ++i) {
-      const int q = tid + 256 * i;
-      if (Q * KR % 256 == 0 || q < Q * KR) {
-        put(Bs, nB, q / KR * LB + (q % KR) * E, rb[i]);
-        if (!STATES) put(Cs, nC, q / KR * LC + (q % KR) * E, rc[i]);
-      }
+    for (int i = 0; i < NKV; ++i) {
+      if (Q * KR % 256 != 0 && kj + i * KS >= Q) continue;
+      put(Bs, nB, (kj + i * KS) * LB + kk, rb[i]);
+      if (!STATES) put(Cs, nC, (kj + i * KS) * LC + kk, rc[i]);
     }
     if (!STATES && weird) bad_[c & 1] = 1;
-    // log-decays: one token per lane
-    const float dtv = lane < here ? softplus(rdt + bias) : 0.f;
-    const double l = wave_prefix((double)fmaxf(rate * dtv, -kMaxDecay) * (lane < here ? kLog2e : 0.0));
-    const double end = __shfl(l, 63, 64);
-    if (wave == 0 && lane < Q) {
-      l_[lane] = l;
-      dtv_[lane] = dtv;
-      left_[lane] = exp2_of(end - l) * dtv;
-    }
-    total += end;
     if (c + 1 < c1) fetch(c + 1);
     __syncthreads();
+    const double* lc = l_[c & 1];
+    const double end = lc[Q - 1];
+    total += end;
 
     if (!STATES) {
       if (tid == 0) bad_[(c + 1) & 1] = 0;
-      // M, tiles (it, jt) on and below the diagonal in turn over the waves
-#pragma unroll 1
-      for (int e = wave; e < QT * (QT + 1) / 2; e += 4) {
-        int it = 0, jt = e;
-        while (jt > it) {
-          ++it;
-          jt -= it;
-        }
-        f32x4_t G = {0.f, 0.f, 0.f, 0.f};
+      // M, tiles (it, jt) on and below the diagonal in turn over the waves; a wave without one more
+      // repeats the last
+      constexpr int MT = QT * (QT + 1) / 2, MW = (MT + 3) / 4;
+      f32x4_t G[MW];
+      int it_[MW], jt_[MW];
 #pragma unroll
-        for (int k = 0; k < NK; ++k)
-          mma(G, along<NP>(Bs + 16 * jt * LB + 32 * k, LB, nB, lane), along<NP>(Cs + 16 * it * LC + 32 * k, LC, nC, lane));
-        const int i = 16 * it + lr, j = 16 * jt + 4 * lg;
-        const double li = l_[i];
+      for (int e = 0; e < MW; ++e) {
+        int it = 0, jt = min(wave + 4 * e, MT - 1);
+        while (jt > it) jt -= ++it;
+        it_[e] = it;
+        jt_[e] = jt;
+        G[e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int k = 0; k < NK; ++k)
+#pragma unroll
+        for (int e = 0; e < MW; ++e)
+          mma(G[e], along<NP>(Bs + 16 * jt_[e] * LB + 32 * k, LB, nB, lane),
+              along<NP>(Cs + 16 * it_[e] * LC + 32 * k, LC, nC, lane));
+#pragma unroll
+      for (int e = 0; e < MW; ++e) {
+        const int i = 16 * it_[e] + lr, j = 16 * jt_[e] + 4 * lg;
+        const double li = lc[i];
         float mv[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mv[u] = j + u <= i ? G[u] * (exp2_of(li - l_[j + u]) * dtv_[j + u]) : 0.f;
+        for (int u = 0; u < 4; ++u) mv[u] = j + u <= i ? G[e][u] * (exp2_of(li - lc[j + u]) * dtv_[c & 1][j + u]) : 0.f;
         uint32_t w0[3], w1[3];
         split_pair(mv[0], mv[1], w0);
         split_pair(mv[2], mv[3], w1);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) *(uint2*)(Ms + k * nM + i * LM + j) = make_uint2(w0[k], w1[k]);
+        for (int k = 0; k < 3; ++k)
+          *(uint2*)(Ms + k * nM + i * LM + across_order(j)) = make_uint2(w0[k], w1[k]);
       }
       Frag<3> Sf[NK];
 #pragma unroll
@@ -228,7 +243,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
 #pragma unroll
         for (int k = 0; k < NK; ++k) mma(y, Sf[k], along<NP>(Cs + 16 * it * LC + 32 * k, LC, nC, lane));
         const int i = 16 * it + lr;
-        y *= exp2_of(l_[i]);
+        y *= exp2_of(lc[i]);
         if (!bad) {
 #pragma unroll
           for (int k = 0; k <= it / 2; ++k) mma(y, xf[k], along<3>(Ms + 16 * it * LM + 32 * k, LM, nM, lane));
@@ -243,7 +258,8 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
         }
         if (bad)  // an infinity or a NaN times the zeros of M would reach earlier tokens: only j <= i
           for (int j = 0; j <= i; ++j) {
-            const float m = bf16_to_f32(Ms[i * LM + j]) + bf16_to_f32(Ms[nM + i * LM + j]) + bf16_to_f32(Ms[2 * nM + i * LM + j]);
+            const uint16_t* mp = Ms + i * LM + across_order(j);
+            const float m = bf16_to_f32(mp[0]) + bf16_to_f32(mp[nM]) + bf16_to_f32(mp[2 * nM]);
             for (int k = NP - 1; k >= 0; --k) {
               const uint2 q = *(const uint2*)(Xs + k * nX + j * LX + 16 * wave + 4 * lg);
               y[0] = fmaf(m, bf16lo(q.x), y[0]);
@@ -260,6 +276,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
         }
       }
     }
+    if (wave == 0 && c + 1 < c1) gates(c + 1);
     // the state at the block's end
     const float keep = exp2_of(end);
 #pragma unroll
@@ -270,19 +287,19 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
       values_of(across<NP>(Xs + 32 * k * LX + 16 * wave, LX, nX, lane), v);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        v[u] *= left_[32 * k + 4 * lg + u];
-        v[4 + u] *= left_[32 * k + 16 + 4 * lg + u];
+        v[u] *= left_[c & 1][32 * k + 4 * lg + u];
+        v[4 + u] *= left_[c & 1][32 * k + 16 + 4 * lg + u];
       }
       const Frag<3> xw = split8(v);
 #pragma unroll
-      for (int m = 0; m < NT; ++m) mma(S[m], across<NP>(Bs + 32 * k * LB + 16 * m, LB, nB, lane), xw);
+      for (int m = 0; m < NT; ++m) mma(S[m], across<NP, 8>(Bs + 32 * k * LB + 32 * (m >> 1) + 4 * (m & 1), LB, nB, lane), xw);
     }
   }
   float* to = STATES ? W.first + (long long)(seg + 1) * A.B * A.H * P * N : seg + 1 == L.segments ? A.s_out : nullptr;
   if (to && p < P) {
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
-      const int k = 16 * m + 4 * lg;
+      const int k = state_at(m);
       if (k < N) *(f32x4_t*)(to + srow + k) = S[m];
     }
   }
@@ -358,12 +375,12 @@ size_t workspace(const sdm_scan_shape& S, const ScanPlan& L, char* base, ScanWs*
 
 template <bool BF16, int NK>
 hipError_t launch_blocks(const ScanArgs& A, const ScanPlan& L, const ScanWs& W, hipStream_t stream) {
-  constexpr int lds = Tiles<BF16, NK>::bytes;
+  constexpr int lds = Tiles<BF16, NK>::bytes, states_lds = Tiles<BF16, NK>::states_bytes;
   const long long units = (long long)A.B * A.H * L.pblocks;
   hipError_t e;
   if (L.segments > 1) {
-    hipLaunchKernelGGL((scan_kernel<BF16, NK, true>), dim3((unsigned)(units * (L.segments - 1))), dim3(256), lds, stream,
-                       A, L, W);
+    hipLaunchKernelGGL((scan_kernel<BF16, NK, true>), dim3((unsigned)(units * (L.segments - 1))), dim3(256),
+                       states_lds, stream, A, L, W);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const long long quads = (long long)A.B * A.H * A.P * A.N / 4;

@@ -91,29 +91,28 @@ __device__ __forceinline__ void mma(f32x4_t& d, const Frag<NA>& a, const Frag<NB
                                                     __builtin_bit_cast(bf16x8_t, b.v[j]), d, 0, 0, 0);
 }
 
-// Reads of fragments from a tile in LDS, rows `ld` bf16 apart, planes (pieces) `plane` apart. The k of a
-// lane with g = l / 16 are 4g..4g+3 and 16+4g..16+4g+3 of the 32: the order in which a lane holds two
-// stacked 16x16 results, which so become operands without leaving their lanes.
+// Reads of fragments from a tile in LDS, rows `ld` bf16 apart, planes (pieces) `plane` apart.
 //
-// along(): row l % 16 of the tile is the operand's row, k runs along it
+// along(): row l % 16 of the tile is the operand's row, k runs along it: lanes with g = l / 16 take the
+// 8 k from 8 g.
 template <int NP>
 __device__ __forceinline__ Frag<NP> along(const uint16_t* tile, int ld, int plane, int lane) {
   Frag<NP> f;
-  const uint16_t* p = tile + (lane & 15) * ld + (lane >> 4) * 4;
+  const uint16_t* p = tile + (lane & 15) * ld + (lane >> 4) * 8;
 #pragma unroll
-  for (int k = 0; k < NP; ++k) {
-    const uint2 a = *(const uint2*)(p + k * plane), b = *(const uint2*)(p + k * plane + 16);
-    f.v[k] = make_uint4(a.x, a.y, b.x, b.y);
-  }
+  for (int k = 0; k < NP; ++k) f.v[k] = *(const uint4*)(p + k * plane);
   return f;
 }
-// across(): column l % 16 of the tile is the operand's row, k runs over the tile's rows. The transposing
-// read hands 16 lanes the columns of four rows of 16 values, whose quarters the lanes address.
-template <int NP>
+// across(): a column of the tile is the operand's row, k runs over the tile's rows: lanes with g = l / 16
+// take rows 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3. The transposing read hands 16 lanes the columns of
+// four rows of four runs of 4 values, which the lanes address. RUN = 4: lane l has column l % 16.
+// RUN = 8: column 8 ((l % 16) / 4) + l % 4, so that this tile and the one 4 columns on are the even and
+// the odd 16 rows of a result whose lanes, with the two stacked, hold the 8 consecutive k of along().
+template <int NP, int RUN = 4>
 __device__ __forceinline__ Frag<NP> across(uint16_t* tile, int ld, int plane, int lane) {
   typedef __attribute__((address_space(3))) s16x4_t lds_t;
   Frag<NP> f;
-  uint16_t* p = tile + ((lane >> 4) * 4 + ((lane >> 2) & 3)) * ld + (lane & 3) * 4;
+  uint16_t* p = tile + ((lane >> 4) * 4 + ((lane >> 2) & 3)) * ld + (lane & 3) * RUN;
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
     const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(p + k * plane)));
@@ -123,16 +122,39 @@ __device__ __forceinline__ Frag<NP> across(uint16_t* tile, int ld, int plane, in
   }
   return f;
 }
+// Where column j of a block of 32 lies in a tile whose rows along() reads against rows that across()
+// reads: the order of across() in runs of 4.
+__device__ __forceinline__ int across_order(int j) {
+  return (j & ~31) | ((j & 12) << 1) | ((j & 16) >> 2) | (j & 3);
+}
 
-// Inclusive sum over the lanes up to this one
+// One step of a prefix sum: v plus the v that the DPP control hands this lane (0 where none, or where
+// the row is not in ROWS)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, true);
+  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Inclusive sum over the lanes up to this one: shifts by 1, 2, 4, 8 in the rows of 16 lanes, then the
+// last lane of row 0 to row 1 and of row 2 to row 3, then lane 31 to rows 2 and 3
 __device__ __forceinline__ double wave_prefix(double v) {
-  const int lane = lane_id();
-#pragma unroll
-  for (int m = 1; m < kWave; m <<= 1) {
-    const double o = __shfl_up(v, m, kWave);
-    if (lane >= m) v += o;
-  }
-  return v;
+  v = add_dpp<0x111, 0xF>(v);
+  v = add_dpp<0x112, 0xF>(v);
+  v = add_dpp<0x114, 0xF>(v);
+  v = add_dpp<0x118, 0xF>(v);
+  v = add_dpp<0x142, 0xA>(v);
+  return add_dpp<0x143, 0xC>(v);
+}
+
+// Lane 63's value in every lane
+__device__ __forceinline__ double last_lane(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
 }  // namespace sdm

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
       if (!STATES) put(Cs, nC, (kj + i * KS) * LC + kk, rc[i]);
     }
     if (!STATES && weird) bad_[c & 1] = 1;
-    if (c + 1 < c1) fetch(c + 1);
+    if (STATES && c + 1 < c1) fetch(c + 1);
     __syncthreads();
     const double* lc = l_[c & 1];
     const double end = lc[Q - 1];
@@ -225,23 +225,26 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
         for (int k = 0; k < 3; ++k)
           *(uint2*)(Ms + k * nM + i * LM + across_order(j)) = make_uint2(w0[k], w1[k]);
       }
-      Frag<3> Sf[NK];
+      __syncthreads();
+      const bool bad = bad_[c & 1] != 0;
+      f32x4_t Y[QT];
+#pragma unroll
+      for (int it = 0; it < QT; ++it) Y[it] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
         const float v[8] = {S[2 * k][0], S[2 * k][1], S[2 * k][2], S[2 * k][3],
                             S[2 * k + 1][0], S[2 * k + 1][1], S[2 * k + 1][2], S[2 * k + 1][3]};
-        Sf[k] = split8(v);
+        const Frag<3> Sf = split8(v);
+#pragma unroll
+        for (int it = 0; it < QT; ++it) mma(Y[it], Sf, along<NP>(Cs + 16 * it * LC + 32 * k, LC, nC, lane));
       }
-      __syncthreads();
-      const bool bad = bad_[c & 1] != 0;
+      if (c + 1 < c1) fetch(c + 1);
       Frag<NP> xf[Q / 32];
 #pragma unroll
       for (int k = 0; k < Q / 32; ++k) xf[k] = across<NP>(Xs + 32 * k * LX + 16 * wave, LX, nX, lane);
 #pragma unroll
       for (int it = 0; it < QT; ++it) {
-        f32x4_t y = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < NK; ++k) mma(y, Sf[k], along<NP>(Cs + 16 * it * LC + 32 * k, LC, nC, lane));
+        f32x4_t y = Y[it];
         const int i = 16 * it + lr;
         y *= exp2_of(lc[i]);
         if (!bad) {

@@ -5,8 +5,8 @@
 //   S_t = a_t S_{t-1} + dtv_t x_t B_t^T,   o_t = S_t C_t + D x_t
 //
 // Prompts run in blocks of Q tokens. With l the log-decay summed from the block's start, S the state
-// before the block and M_ij = (C_i . B_j) exp(l_i - l_j) dtv_j for j <= i:
-//   o_i = exp(l_i) S C_i + sum_j M_ij x_j + D x_i
+// before the block and M_ij = (C_i . B_j) exp(l_i - l_j) dtv_j for j <= i, D more for j = i:
+//   o_i = exp(l_i) S C_i + sum_j M_ij x_j
 //   S'  = exp(l_end) S + sum_j (exp(l_end - l_j) dtv_j x_j) B_j^T
 // all of them matrix products. l is summed in float64, so that the differences keep their digits.
 
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   constexpr int Q = TL::Q, NP = TL::NP, NT = 2 * NK, QT = Q / 16;
   constexpr int LB = TL::LB, LC = TL::LC, LX = TL::LX, LM = TL::LM, nB = TL::nB, nC = TL::nC, nX = TL::nX, nM = TL::nM;
   extern __shared__ __align__(16) uint16_t lds[];
-  __shared__ double l_[2][Q];
+  __shared__ __align__(16) double l_[2][Q];
   __shared__ __align__(16) float dtv_[2][Q], left_[2][Q];
   __shared__ int bad_[2];  // does x of the block hold an infinity or a NaN, by the block's parity
   uint16_t *Bs = lds, *Xs = Bs + NP * nB, *Cs = Xs + NP * nX, *Ms = Cs + NP * nC;
@@ -84,27 +84,46 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   const uint32_t xoff = (uint32_t)(xj * A.ld_x + xk) * ES, boff = (uint32_t)(kj * A.ld_b + kk) * ES,
                  coff = (uint32_t)(kj * A.ld_c + kk) * ES;
   uint4 rx[NX], rb[NKV], rc[NKV];
-  float rdt = 0.f;
-  auto fetch = [&](int c) {
+  const bool wide = p0 + kPB <= P && N == NK * 32;  // every column of the tiles is there
+  // part `part` of `parts` of a block's pieces
+  auto fetch = [&](int c, int part, int parts) {
     const int t0 = c * Q, here = min(max(n - t0, 0), Q);
     const long long row0 = (long long)b * A.T + t0;
     const char* px = (const char*)A.x + (row0 * A.ld_x + h * P + p0) * ES;
     const char* pb_ = (const char*)A.Bm + (row0 * A.ld_b + g * N) * ES;
     const char* pc = (const char*)A.Cm + (row0 * A.ld_c + g * N) * ES;
-    const int xrows = xin ? here : 0, krows = kin ? here : 0;
+    if (wide && here == Q && Q * KR % 256 == 0) {
 #pragma unroll
-    for (int i = 0; i < NX; ++i)
-      rx[i] = xj + i * XS < xrows ? *(const uint4*)(px + i * XS * A.ld_x * ES + xoff) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < NKV; ++i)
+        if (i % parts == part) {
+          rb[i] = *(const uint4*)(pb_ + i * KS * A.ld_b * ES + boff);
+          if (!STATES) rc[i] = *(const uint4*)(pc + i * KS * A.ld_c * ES + coff);
+        }
 #pragma unroll
-    for (int i = 0; i < NKV; ++i) {
-      const bool in = kj + i * KS < krows;
-      rb[i] = in ? *(const uint4*)(pb_ + i * KS * A.ld_b * ES + boff) : make_uint4(0u, 0u, 0u, 0u);
-      if (!STATES) rc[i] = in ? *(const uint4*)(pc + i * KS * A.ld_c * ES + coff) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < NX; ++i)
+        if (i % parts == part) rx[i] = *(const uint4*)(px + i * XS * A.ld_x * ES + xoff);
+    } else {
+      const int xrows = xin ? here : 0, krows = kin ? here : 0;
+#pragma unroll
+      for (int i = 0; i < NKV; ++i)
+        if (i % parts == part) {
+          const bool in = kj + i * KS < krows;
+          rb[i] = in ? *(const uint4*)(pb_ + i * KS * A.ld_b * ES + boff) : make_uint4(0u, 0u, 0u, 0u);
+          if (!STATES) rc[i] = in ? *(const uint4*)(pc + i * KS * A.ld_c * ES + coff) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+      for (int i = 0; i < NX; ++i)
+        if (i % parts == part)
+          rx[i] = xj + i * XS < xrows ? *(const uint4*)(px + i * XS * A.ld_x * ES + xoff) : make_uint4(0u, 0u, 0u, 0u);
     }
-    if (wave == 0) rdt = lane < here ? A.dt[(row0 + lane) * A.ld_dt + h] : 0.f;
   };
-  // log-decays of a block by wave 0, one token per lane, into the arrays of the block's parity
-  auto gates = [&](int c) {
+  // dt of a block, one token per lane of the wave that forms its log-decays; read two blocks ahead
+  auto fetch_dt = [&](int c) {
+    const int here = min(max(n - c * Q, 0), Q);
+    return lane < here ? A.dt[((long long)b * A.T + c * Q + lane) * A.ld_dt + h] : 0.f;
+  };
+  // log-decays of a block, one token per lane, into the arrays of the block's parity
+  auto gates = [&](int c, float rdt) {
     const int here = min(max(n - c * Q, 0), Q);
     const float dtv = lane < here ? softplus(rdt + bias) : 0.f;
     const double l = wave_prefix((double)fmaxf(rate * dtv, -kMaxDecay) * (lane < here ? kLog2e : 0.0));
@@ -157,8 +176,13 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   if (!STATES)  // the tiles of M right of the diagonal stay 0
     for (int i = tid; i < 3 * nM / 8; i += 256) ((uint4*)Ms)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (tid == 0) bad_[c0 & 1] = 0;
-  fetch(c0);
-  if (wave == 0) gates(c0);
+  float rdt = 0.f;  // dt of block c + 1 at the start of block c
+  if (wave == 3) {
+    const float first = fetch_dt(c0);
+    rdt = fetch_dt(c0 + 1);
+    gates(c0, first);
+  }
+  fetch(c0, 0, 1);
   for (int c = c0; c < c1; ++c) {
     const int t0 = c * Q, here = min(max(n - t0, 0), Q), rows = min(A.T - t0, Q);
     float* orow = STATES ? nullptr : A.o + (bh * A.T + t0) * P + p0;
@@ -184,11 +208,33 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
       if (!STATES) put(Cs, nC, (kj + i * KS) * LC + kk, rc[i]);
     }
     if (!STATES && weird) bad_[c & 1] = 1;
-    if (STATES && c + 1 < c1) fetch(c + 1);
+    if (STATES && c + 1 < c1) fetch(c + 1, 0, 1);
     __syncthreads();
+    if (wave == 3) {  // (the wave with the fewest tiles of M)
+      gates(c + 1, rdt);
+      rdt = fetch_dt(c + 2);
+    }
     const double* lc = l_[c & 1];
     const double end = lc[Q - 1];
     total += end;
+
+    // x of this wave's channels, tokens along k; and weighted for the state at the block's end
+    const float keep = exp2_of(end);
+    Frag<NP> xf[Q / 32];
+    Frag<3> xw[Q / 32];
+    auto load_x = [&] {
+#pragma unroll
+      for (int k = 0; k < Q / 32; ++k) xf[k] = across<NP>(Xs + 32 * k * LX + 16 * wave, LX, nX, lane);
+    };
+    auto weigh_x = [&](int k) {
+      float v[8];
+      values_of(xf[k], v);
+      const float4 w0 = *(const float4*)(left_[c & 1] + 32 * k + 4 * lg), w1 = *(const float4*)(left_[c & 1] + 32 * k + 16 + 4 * lg);
+      const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] *= w[u];
+      xw[k] = split8(v);
+    };
 
     if (!STATES) {
       if (tid == 0) bad_[(c + 1) & 1] = 0;
@@ -205,19 +251,38 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
         jt_[e] = jt;
         G[e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
+      Frag<NP> gb[2][MW], gc[2][MW];
+      auto load_g = [&](int k) {
 #pragma unroll
-      for (int k = 0; k < NK; ++k)
+        for (int e = 0; e < MW; ++e) {
+          gb[k & 1][e] = along<NP>(Bs + 16 * jt_[e] * LB + 32 * k, LB, nB, lane);
+          gc[k & 1][e] = along<NP>(Cs + 16 * it_[e] * LC + 32 * k, LC, nC, lane);
+        }
+      };
+      load_g(0);
 #pragma unroll
-        for (int e = 0; e < MW; ++e)
-          mma(G[e], along<NP>(Bs + 16 * jt_[e] * LB + 32 * k, LB, nB, lane),
-              along<NP>(Cs + 16 * it_[e] * LC + 32 * k, LC, nC, lane));
+      for (int k = 0; k < NK; ++k) {
+        if (k + 1 < NK) load_g(k + 1);
+        stage();
+#pragma unroll
+        for (int e = 0; e < MW; ++e) mma(G[e], gb[k & 1][e], gc[k & 1][e]);
+      }
 #pragma unroll
       for (int e = 0; e < MW; ++e) {
         const int i = 16 * it_[e] + lr, j = 16 * jt_[e] + 4 * lg;
         const double li = lc[i];
+        const double2 l0 = *(const double2*)(lc + j), l1 = *(const double2*)(lc + j + 2);
+        const float4 d4 = *(const float4*)(dtv_[c & 1] + j);
+        const double lj[4] = {l0.x, l0.y, l1.x, l1.y};
+        const float dj[4] = {d4.x, d4.y, d4.z, d4.w};
         float mv[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mv[u] = j + u <= i ? G[e][u] * (exp2_of(li - lc[j + u]) * dtv_[c & 1][j + u]) : 0.f;
+        for (int u = 0; u < 4; ++u) {
+          // right of the diagonal whatever the product is gives 0, by its bits: no branch around the exp
+          const float v = G[e][u] * (exp2_of(li - lj[u]) * dj[u]);
+          mv[u] = __uint_as_float(__float_as_uint(v) & (j + u <= i ? ~0u : 0u)) +
+                  __uint_as_float(__float_as_uint(D) & (j + u == i ? ~0u : 0u));
+        }
         uint32_t w0[3], w1[3];
         split_pair(mv[0], mv[1], w0);
         split_pair(mv[2], mv[3], w1);
@@ -225,77 +290,103 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
         for (int k = 0; k < 3; ++k)
           *(uint2*)(Ms + k * nM + i * LM + across_order(j)) = make_uint2(w0[k], w1[k]);
       }
-      __syncthreads();
-      const bool bad = bad_[c & 1] != 0;
       f32x4_t Y[QT];
+      Frag<NP> cf[2][QT];
+      auto load_c = [&](int k) {
+#pragma unroll
+        for (int it = 0; it < QT; ++it) cf[k & 1][it] = along<NP>(Cs + 16 * it * LC + 32 * k, LC, nC, lane);
+      };
+      load_c(0);
 #pragma unroll
       for (int it = 0; it < QT; ++it) Y[it] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < NK; ++k) {
+      Frag<3> Sf[2];
+      auto split_s = [&](int k) {  // the pieces of 32 d_k of the state, which then decays to the block's end
         const float v[8] = {S[2 * k][0], S[2 * k][1], S[2 * k][2], S[2 * k][3],
                             S[2 * k + 1][0], S[2 * k + 1][1], S[2 * k + 1][2], S[2 * k + 1][3]};
-        const Frag<3> Sf = split8(v);
+        Sf[k & 1] = split8(v);
+        S[2 * k] *= keep;
+        S[2 * k + 1] *= keep;
+      };
+      split_s(0);
+      __syncthreads();
+      const bool bad = bad_[c & 1] != 0;
 #pragma unroll
-        for (int it = 0; it < QT; ++it) mma(Y[it], Sf, along<NP>(Cs + 16 * it * LC + 32 * k, LC, nC, lane));
+      for (int k = 0; k < NK; ++k) {
+        if (k + 1 < NK) load_c(k + 1);
+        if (c + 1 < c1) fetch(c + 1, k, NK);
+        stage();
+        if (k + 1 < NK) split_s(k + 1);
+        mma_rows<QT>(Y, Sf[k & 1], cf[k & 1]);
+        interleave<QT * 3 * (NP == 1 ? 1 : 2), NP == 1 ? 5 : 3>();
+        stage();
       }
-      if (c + 1 < c1) fetch(c + 1);
-      Frag<NP> xf[Q / 32];
 #pragma unroll
-      for (int k = 0; k < Q / 32; ++k) xf[k] = across<NP>(Xs + 32 * k * LX + 16 * wave, LX, nX, lane);
+      for (int it = 0; it < QT; ++it) Y[it] *= exp2_of(lc[16 * it + lr]);
+      if (!bad) {
 #pragma unroll
-      for (int it = 0; it < QT; ++it) {
-        f32x4_t y = Y[it];
-        const int i = 16 * it + lr;
-        y *= exp2_of(lc[i]);
-        if (!bad) {
+        for (int k = 0; k < Q / 32; ++k) {  // token tiles from 2 k on
+          Frag<3> mf[QT];
+          if (k == 0) load_x();
 #pragma unroll
-          for (int k = 0; k <= it / 2; ++k) mma(y, xf[k], along<3>(Ms + 16 * it * LM + 32 * k, LM, nM, lane));
+          for (int it = 2 * k; it < QT; ++it) mf[it] = along<3>(Ms + 16 * it * LM + 32 * k, LM, nM, lane);
+          stage();
+          weigh_x(k);
+          if (k == 0) mma_rows<QT>(Y, xf[k], mf);
+          else mma_rows<QT - 2>(Y + 2, xf[k], mf + 2);
+          interleave<(QT - 2) * 3, 10>();
+          stage();
         }
-        float xi[4] = {0.f, 0.f, 0.f, 0.f};  // channels 4 lg .. of this wave, token i
-        for (int k = NP - 1; k >= 0; --k) {
-          const uint2 q = *(const uint2*)(Xs + k * nX + i * LX + 16 * wave + 4 * lg);
-          xi[0] += bf16lo(q.x);
-          xi[1] += bf16hi(q.x);
-          xi[2] += bf16lo(q.y);
-          xi[3] += bf16hi(q.y);
-        }
-        if (bad)  // an infinity or a NaN times the zeros of M would reach earlier tokens: only j <= i
-          for (int j = 0; j <= i; ++j) {
-            const uint16_t* mp = Ms + i * LM + across_order(j);
+      } else {  // an infinity or a NaN times the zeros of M would reach earlier tokens: only j <= i
+        load_x();
+#pragma unroll
+        for (int k = 0; k < Q / 32; ++k) weigh_x(k);
+#pragma unroll
+        for (int it = 0; it < QT; ++it)
+          for (int j = 0; j <= 16 * it + lr; ++j) {
+            const uint16_t* mp = Ms + (16 * it + lr) * LM + across_order(j);
             const float m = bf16_to_f32(mp[0]) + bf16_to_f32(mp[nM]) + bf16_to_f32(mp[2 * nM]);
             for (int k = NP - 1; k >= 0; --k) {
               const uint2 q = *(const uint2*)(Xs + k * nX + j * LX + 16 * wave + 4 * lg);
-              y[0] = fmaf(m, bf16lo(q.x), y[0]);
-              y[1] = fmaf(m, bf16hi(q.x), y[1]);
-              y[2] = fmaf(m, bf16lo(q.y), y[2]);
-              y[3] = fmaf(m, bf16hi(q.y), y[3]);
+              Y[it][0] = fmaf(m, bf16lo(q.x), Y[it][0]);
+              Y[it][1] = fmaf(m, bf16hi(q.x), Y[it][1]);
+              Y[it][2] = fmaf(m, bf16lo(q.y), Y[it][2]);
+              Y[it][3] = fmaf(m, bf16hi(q.y), Y[it][3]);
             }
           }
-        const int k = 16 * wave + 4 * lg;
-        if (i < rows && p0 + k < P) {
-          float4 v = make_float4(fmaf(D, xi[0], y[0]), fmaf(D, xi[1], y[1]), fmaf(D, xi[2], y[2]), fmaf(D, xi[3], y[3]));
-          if (i >= here) v = make_float4(0.f, 0.f, 0.f, 0.f);
-          *(float4*)(orow + (long long)i * P + k) = v;
-        }
+      }
+      float* oo = orow + (long long)lr * P + 16 * wave + 4 * lg;
+      if (wide && here == Q) {
+#pragma unroll
+        for (int it = 0; it < QT; ++it) *(f32x4_t*)(oo + 16 * it * P) = Y[it];
+      } else if (p0 + 16 * wave + 4 * lg < P) {
+#pragma unroll
+        for (int it = 0; it < QT; ++it)
+          if (16 * it + lr < rows)
+            *(f32x4_t*)(oo + 16 * it * P) = 16 * it + lr < here ? Y[it] : f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
     }
-    if (wave == 0 && c + 1 < c1) gates(c + 1);
     // the state at the block's end
-    const float keep = exp2_of(end);
+    if (STATES) {
+      load_x();
 #pragma unroll
-    for (int m = 0; m < NT; ++m) S[m] *= keep;
+      for (int k = 0; k < Q / 32; ++k) weigh_x(k);
 #pragma unroll
-    for (int k = 0; k < Q / 32; ++k) {
-      float v[8];
-      values_of(across<NP>(Xs + 32 * k * LX + 16 * wave, LX, nX, lane), v);
+      for (int m = 0; m < NT; ++m) S[m] *= keep;
+    }
+    constexpr int MH = NT < 4 ? NT : 4;  // tiles of d_k at a time
+    Frag<NP> bf[2][MH];
+    auto load_b = [&](int s) {  // step s: 32 tokens, MH tiles
+      const int k = s / (NT / MH), m0 = s % (NT / MH) * MH;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        v[u] *= left_[c & 1][32 * k + 4 * lg + u];
-        v[4 + u] *= left_[c & 1][32 * k + 16 + 4 * lg + u];
-      }
-      const Frag<3> xw = split8(v);
+      for (int m = 0; m < MH; ++m)
+        bf[s & 1][m] = across<NP, 8>(Bs + 32 * k * LB + 32 * ((m0 + m) >> 1) + 4 * (m & 1), LB, nB, lane);
+    };
+    load_b(0);
 #pragma unroll
-      for (int m = 0; m < NT; ++m) mma(S[m], across<NP, 8>(Bs + 32 * k * LB + 32 * (m >> 1) + 4 * (m & 1), LB, nB, lane), xw);
+    for (int s = 0; s < Q / 32 * (NT / MH); ++s) {
+      if (s + 1 < Q / 32 * (NT / MH)) load_b(s + 1);
+      stage();
+      mma_cols<MH>(S + s % (NT / MH) * MH, bf[s & 1], xw[s / (NT / MH)]);
     }
   }
   float* to = STATES ? W.first + (long long)(seg + 1) * A.B * A.H * P * N : seg + 1 == L.segments ? A.s_out : nullptr;

@@ -91,6 +91,47 @@ __device__ __forceinline__ void mma(f32x4_t& d, const Frag<NA>& a, const Frag<NB
                                                     __builtin_bit_cast(bf16x8_t, b.v[j]), d, 0, 0, 0);
 }
 
+// The same for N results at once with one common operand each way: neighbouring instructions add to
+// different results, so none waits for the one before. d[i] += a_i b_i with a or b the same for all.
+template <int N, int NA, int NB>
+__device__ __forceinline__ void mma_rows(f32x4_t* d, const Frag<NA>& a, const Frag<NB>* b) {
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = NB - 1; j >= 0; --j)
+#pragma unroll
+      for (int r = 0; r < N; ++r)
+        if (i + j <= 2)
+          d[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a.v[i]),
+                                                         __builtin_bit_cast(bf16x8_t, b[r].v[j]), d[r], 0, 0, 0);
+}
+template <int N, int NA, int NB>
+__device__ __forceinline__ void mma_cols(f32x4_t* d, const Frag<NA>* a, const Frag<NB>& b) {
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = NB - 1; j >= 0; --j)
+#pragma unroll
+      for (int r = 0; r < N; ++r)
+        if (i + j <= 2)
+          d[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a[r].v[i]),
+                                                         __builtin_bit_cast(bf16x8_t, b.v[j]), d[r], 0, 0, 0);
+}
+
+// Keeps reads that are written ahead of the products of the step before ahead of them
+__device__ __forceinline__ void stage() { __builtin_amdgcn_sched_barrier(0); }
+
+// Asks for an order of `M` matrix instructions with V vector instructions behind each: a wave issues in
+// order, so only what is written between them runs beside them
+template <int M, int V>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+  }
+}
+
 // Reads of fragments from a tile in LDS, rows `ld` bf16 apart, planes (pieces) `plane` apart.
 //
 // along(): row l % 16 of the tile is the operand's row, k runs along it: lanes with g = l / 16 take the

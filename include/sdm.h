@@ -447,7 +447,7 @@ sdm_status sdm_short_conv_backward(const sdm_conv_shape* shape, const void* x, c
 /* Shape of the selective scan. B, H >= 1, T >= 0; G >= 1 divides H (head h reads group
  * h / (H/G)); d_k and d_v >= 1 multiples of 8 with d_k <= 128 and d_v <= 256 (else
  * SDM_ERR_UNSUPPORTED); ld_x >= H*d_v, ld_b, ld_c >= G*d_k, multiples of 8; ld_dt >= H;
- * B*T <= 2^30 - 1, B*H <= 65535, H <= 4096, token strides <= 2^22. */
+ * B*T <= 2^29 - 1, B*H <= 65535, H <= 4096, token strides <= 2^22. */
 typedef struct {
   int32_t B, T;       /* sequences, tokens per sequence in this call               */
   int32_t H, G;       /* heads, groups of heads that share B and C                 */
@@ -458,9 +458,9 @@ typedef struct {
 
 sdm_status sdm_check_scan_shape(const sdm_scan_shape* shape);
 
-/* Bytes of device memory sdm_selective_scan needs as workspace: the states at the starts of
- * the token segments that a call with few heads is split into (0 if it is not split, or if the
- * shape is invalid). */
+/* Bytes of device memory sdm_selective_scan needs as workspace: 20 bytes per token and head of
+ * time steps and decays, and the states at the starts of the token segments that a call with
+ * few heads is split into. 0 if the shape is invalid. */
 size_t sdm_selective_scan_workspace_bytes(const sdm_scan_shape* shape);
 
 /* Selective state space scan. For each sequence and head, tokens in order:
@@ -476,8 +476,8 @@ size_t sdm_selective_scan_workspace_bytes(const sdm_scan_shape* shape);
  * bf16 pieces that add up to it exactly, and sums are float32; log-decays are added up in
  * float64 (and floored at -1000 per token, a decay of 0 in float32). A NaN or an infinity at a
  * token reaches no earlier token's output.
- * ws: at least sdm_selective_scan_workspace_bytes(shape) bytes (may be NULL if that is 0),
- * apart from every other buffer and not shared with a call that may run at the same time. */
+ * ws: at least sdm_selective_scan_workspace_bytes(shape) bytes (may be NULL if T is 0), apart
+ * from every other buffer and not shared with a call that may run at the same time. */
 sdm_status sdm_selective_scan(const sdm_scan_shape* shape, const void* x, const void* Bm, const void* Cm,
                               const float* dt, const float* A_log, const float* dt_bias, const float* D,
                               const int32_t* lengths, const float* s_in, float* s_out, float* o, void* ws,

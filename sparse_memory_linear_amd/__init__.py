@@ -499,7 +499,7 @@ def selective_scan_workspace_bytes(shape: ScanShape) -> int:
     return lib().sdm_selective_scan_workspace_bytes(ctypes.byref(shape))
 
 
-def selective_scan(shape: ScanShape, x, Bm, Cm, dt, A_log, dt_bias, o, ws=None, D=None, lengths=None, s_in=None,
+def selective_scan(shape: ScanShape, x, Bm, Cm, dt, A_log, dt_bias, o, ws, D=None, lengths=None, s_in=None,
                    s_out=None, stream=None):
     s, a = shape, _Args("sdm_selective_scan")
     state = (s.B, s.H, s.d_v, s.d_k)

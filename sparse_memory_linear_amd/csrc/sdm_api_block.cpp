@@ -89,7 +89,7 @@ sdm_status check_scan(const sdm_scan_shape* S) {
   // a block of 64 rows is addressed with 32-bit byte offsets
   if (S->ld_x > kMaxScanStride || S->ld_b > kMaxScanStride || S->ld_c > kMaxScanStride || S->ld_dt > kMaxScanStride)
     return SDM_ERR_UNSUPPORTED;
-  if ((int64_t)S->B * S->T > kMaxTokens || (int64_t)S->B * S->H > 65535) return SDM_ERR_UNSUPPORTED;
+  if ((int64_t)S->B * S->T > (kMaxTokens >> 1) || (int64_t)S->B * S->H > 65535) return SDM_ERR_UNSUPPORTED;
   return SDM_OK;
 }
 

@@ -45,17 +45,49 @@ struct Tiles {
   static constexpr int bytes = (NP * (nB + nX + nC) + 3 * nM) * 2, states_bytes = NP * (nB + nX) * 2;
 };
 
+// ------------------------------------------------------------------ time steps
+// A workgroup takes 64 tokens of a sequence, all heads: dt comes in along the heads, goes through LDS and
+// is summed along the tokens, one per lane.
+template <int Q>
+__global__ void __launch_bounds__(256) scan_gates_kernel(ScanArgs A, ScanGates g) {
+  __shared__ float tile[64][65];
+  const int blocks = g.stride / 64, b = blockIdx.x / blocks, t0 = (int)(blockIdx.x % blocks) * 64;
+  const int here = min(max(sequence_length(A.lengths, b, A.T) - t0, 0), 64);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int h0 = 0; h0 < A.H; h0 += 64) {
+    const int heads = min(A.H - h0, 64);
+    __syncthreads();
+    for (int i = threadIdx.x; i < here * heads; i += 256)
+      tile[i / heads][i % heads] = A.dt[((long long)b * A.T + t0 + i / heads) * A.ld_dt + h0 + i % heads];
+    __syncthreads();
+    for (int h = wave; h < heads; h += 4) {
+      const float step = lane < here ? softplus(tile[lane][h] + A.dt_bias[h0 + h]) : 0.f;
+      const float la = lane < here ? fmaxf(-expf(A.A_log[h0 + h]) * step, -kMaxDecay) : 0.f;
+      const double l = block_prefix<Q>((double)la * kLog2e);
+      const double end = Q == 64 || lane >= 32 ? read_lane(l, 63) : read_lane(l, 31);
+      const long long at = ((long long)b * A.H + h0 + h) * g.stride + t0 + lane;
+      g.l[at] = l;
+      g.step[at] = step;
+      g.since[at] = exp2_of(l);
+      g.left[at] = exp2_of(end - l) * step;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ prompts
 // One workgroup walks the blocks of a segment of a (sequence, head, 64 channels) unit with the state in
 // the accumulators of its matrix products: wave w holds channels 16 w .. 16 w + 15, all d_k.
 // STATES: only the state at the segment's end is wanted (of all segments but the last).
 template <bool BF16, int NK, bool STATES>
-__global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, ScanWs W) {
+__global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, ScanWs W, ScanGates R) {
   using TL = Tiles<BF16, NK>;
   constexpr int Q = TL::Q, NP = TL::NP, NT = 2 * NK, QT = Q / 16;
   constexpr int LB = TL::LB, LC = TL::LC, LX = TL::LX, LM = TL::LM, nB = TL::nB, nC = TL::nC, nX = TL::nX, nM = TL::nM;
   extern __shared__ __align__(16) uint16_t lds[];
-  __shared__ __align__(16) double l_[2][Q];
-  __shared__ __align__(16) float dtv_[2][Q], left_[2][Q];
+  // of the block: log-decays, steps, factors to the token and to the block's end, and for the tiles of M off
+  // the diagonal the factors from the start of a token's tile to it and from a token to the start of tile it
+  __shared__ __align__(16) double l_[Q];
+  __shared__ __align__(16) float step_[Q], since_[Q], left_[Q], up_[Q], down_[QT][Q];
   __shared__ int bad_[2];  // does x of the block hold an infinity or a NaN, by the block's parity
   uint16_t *Bs = lds, *Xs = Bs + NP * nB, *Cs = Xs + NP * nX, *Ms = Cs + NP * nC;
 
@@ -71,7 +103,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   const int n = sequence_length(A.lengths, b, A.T);
   const int N = A.N, P = A.P, p0 = pb * kPB;
   const int c0 = (int)((long long)L.blocks * seg / L.segments), c1 = (int)((long long)L.blocks * (seg + 1) / L.segments);
-  const float rate = -expf(A.A_log[h]), bias = A.dt_bias[h], D = A.D ? A.D[h] : 0.f;
+  const float D = A.D ? A.D[h] : 0.f;
 
   // 16-byte pieces of a block's tiles: piece i of this thread lies in row j + i (256 / pieces-per-row) for
   // its row j of piece 0, in the same columns; `in` is what the columns allow
@@ -117,22 +149,32 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
           rx[i] = xj + i * XS < xrows ? *(const uint4*)(px + i * XS * A.ld_x * ES + xoff) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
-  // dt of a block, one token per lane of the wave that forms its log-decays; read two blocks ahead
-  auto fetch_dt = [&](int c) {
-    const int here = min(max(n - c * Q, 0), Q);
-    return lane < here ? A.dt[((long long)b * A.T + c * Q + lane) * A.ld_dt + h] : 0.f;
+  // the block's gates, one token per lane
+  double rl = 0.0;
+  float rstep = 0.f, rfac = 0.f;
+  auto fetch_gates = [&](int c) {
+    const long long at = bh * R.stride + c * Q + (lane & (Q - 1));
+    rl = R.l[at];
+    if (!STATES) rstep = R.step[at];
+    rfac = (wave == 2 ? R.since : R.left)[at];
   };
-  // log-decays of a block, one token per lane, into the arrays of the block's parity
-  auto gates = [&](int c, float rdt) {
-    const int here = min(max(n - c * Q, 0), Q);
-    const float dtv = lane < here ? softplus(rdt + bias) : 0.f;
-    const double l = wave_prefix((double)fmaxf(rate * dtv, -kMaxDecay) * (lane < here ? kLog2e : 0.0));
-    const double end = last_lane(l);
+  auto put_gates = [&] {
     if (lane < Q) {
-      l_[c & 1][lane] = l;
-      dtv_[c & 1][lane] = dtv;
-      left_[c & 1][lane] = exp2_of(end - l) * dtv;
+      if (wave == 3) left_[lane] = rfac;
+      if (STATES) return;
+      if (wave == 0) l_[lane] = rl;
+      if (wave == 1) step_[lane] = rstep;
+      if (wave == 2) since_[lane] = rfac;
     }
+    if (STATES) return;
+    double from = 0.0;  // log-decay at the start of this lane's tile
+#pragma unroll
+    for (int it = 1; it < QT; ++it) {
+      const double at = read_lane(rl, 16 * it - 1);
+      from = lane >= 16 * it ? at : from;
+      if (wave == it && lane < 16 * it) down_[it][lane] = exp2_of(at - rl) * rstep;
+    }
+    if (wave == 0 && lane < Q) up_[lane] = exp2_of(rl - from);
   };
   // a piece into its tile: as it is, or its four float32 values as three bf16 planes
   auto put = [&](uint16_t* tile, int plane, int at, const uint4& v) {
@@ -176,12 +218,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   if (!STATES)  // the tiles of M right of the diagonal stay 0
     for (int i = tid; i < 3 * nM / 8; i += 256) ((uint4*)Ms)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (tid == 0) bad_[c0 & 1] = 0;
-  float rdt = 0.f;  // dt of block c + 1 at the start of block c
-  if (wave == 3) {
-    const float first = fetch_dt(c0);
-    rdt = fetch_dt(c0 + 1);
-    gates(c0, first);
-  }
+  if (c0 < c1) fetch_gates(c0);
   fetch(c0, 0, 1);
   for (int c = c0; c < c1; ++c) {
     const int t0 = c * Q, here = min(max(n - t0, 0), Q), rows = min(A.T - t0, Q);
@@ -208,16 +245,12 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
       if (!STATES) put(Cs, nC, (kj + i * KS) * LC + kk, rc[i]);
     }
     if (!STATES && weird) bad_[c & 1] = 1;
+    put_gates();
+    const double end = read_lane(rl, Q - 1);
+    total += end;
+    if (c + 1 < c1) fetch_gates(c + 1);
     if (STATES && c + 1 < c1) fetch(c + 1, 0, 1);
     __syncthreads();
-    if (wave == 3) {  // (the wave with the fewest tiles of M)
-      gates(c + 1, rdt);
-      rdt = fetch_dt(c + 2);
-    }
-    const double* lc = l_[c & 1];
-    const double end = lc[Q - 1];
-    total += end;
-
     // x of this wave's channels, tokens along k; and weighted for the state at the block's end
     const float keep = exp2_of(end);
     Frag<NP> xf[Q / 32];
@@ -229,7 +262,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
     auto weigh_x = [&](int k) {
       float v[8];
       values_of(xf[k], v);
-      const float4 w0 = *(const float4*)(left_[c & 1] + 32 * k + 4 * lg), w1 = *(const float4*)(left_[c & 1] + 32 * k + 16 + 4 * lg);
+      const float4 w0 = *(const float4*)(left_ + 32 * k + 4 * lg), w1 = *(const float4*)(left_ + 32 * k + 16 + 4 * lg);
       const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
       for (int u = 0; u < 8; ++u) v[u] *= w[u];
@@ -238,17 +271,18 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
 
     if (!STATES) {
       if (tid == 0) bad_[(c + 1) & 1] = 0;
-      // M, tiles (it, jt) on and below the diagonal in turn over the waves; a wave without one more
+      // M, tiles (it, jt) in turn over the waves, those on the diagonal first; a wave without one more
       // repeats the last
       constexpr int MT = QT * (QT + 1) / 2, MW = (MT + 3) / 4;
       f32x4_t G[MW];
       int it_[MW], jt_[MW];
 #pragma unroll
       for (int e = 0; e < MW; ++e) {
-        int it = 0, jt = min(wave + 4 * e, MT - 1);
-        while (jt > it) jt -= ++it;
-        it_[e] = it;
-        jt_[e] = jt;
+        const int t = min(wave + 4 * e, MT - 1);
+        int it = 1, jt = t - QT;
+        while (jt >= it) jt -= it++;
+        it_[e] = t < QT ? t : it;
+        jt_[e] = t < QT ? t : jt;
         G[e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
       Frag<NP> gb[2][MW], gc[2][MW];
@@ -270,18 +304,24 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
 #pragma unroll
       for (int e = 0; e < MW; ++e) {
         const int i = 16 * it_[e] + lr, j = 16 * jt_[e] + 4 * lg;
-        const double li = lc[i];
-        const double2 l0 = *(const double2*)(lc + j), l1 = *(const double2*)(lc + j + 2);
-        const float4 d4 = *(const float4*)(dtv_[c & 1] + j);
-        const double lj[4] = {l0.x, l0.y, l1.x, l1.y};
-        const float dj[4] = {d4.x, d4.y, d4.z, d4.w};
         float mv[4];
+        if (it_[e] != jt_[e]) {
+          const float up = up_[i];
+          const f32x4_t down = *(const f32x4_t*)(down_[it_[e]] + j);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          // right of the diagonal whatever the product is gives 0, by its bits: no branch around the exp
-          const float v = G[e][u] * (exp2_of(li - lj[u]) * dj[u]);
-          mv[u] = __uint_as_float(__float_as_uint(v) & (j + u <= i ? ~0u : 0u)) +
-                  __uint_as_float(__float_as_uint(D) & (j + u == i ? ~0u : 0u));
+          for (int u = 0; u < 4; ++u) mv[u] = G[e][u] * (up * down[u]);
+        } else {
+          const double li = l_[i];
+          const double2 l0 = *(const double2*)(l_ + j), l1 = *(const double2*)(l_ + j + 2);
+          const f32x4_t step = *(const f32x4_t*)(step_ + j);
+          const double lj[4] = {l0.x, l0.y, l1.x, l1.y};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            // right of the diagonal whatever the product is gives 0, by its bits: no branch around the exp
+            const float v = G[e][u] * (exp2_of(li - lj[u]) * step[u]);
+            mv[u] = __uint_as_float(__float_as_uint(v) & (j + u <= i ? ~0u : 0u)) +
+                    __uint_as_float(__float_as_uint(D) & (j + u == i ? ~0u : 0u));
+          }
         }
         uint32_t w0[3], w1[3];
         split_pair(mv[0], mv[1], w0);
@@ -321,7 +361,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
         stage();
       }
 #pragma unroll
-      for (int it = 0; it < QT; ++it) Y[it] *= exp2_of(lc[16 * it + lr]);
+      for (int it = 0; it < QT; ++it) Y[it] *= since_[16 * it + lr];
       if (!bad) {
 #pragma unroll
         for (int k = 0; k < Q / 32; ++k) {  // token tiles from 2 k on
@@ -459,22 +499,25 @@ ScanPlan plan_of(const sdm_scan_shape& S) {
   return L;
 }
 
-size_t workspace(const sdm_scan_shape& S, const ScanPlan& L, char* base, ScanWs* W) {
-  if (L.segments < 2) return 0;
-  const size_t units = (size_t)S.B * S.H, st = align_up(units * L.segments * S.d_v * S.d_k * 4);
-  W->first = (float*)base;
-  W->decay = (double*)(base + st);
-  return st + align_up(units * L.segments * 8);
+size_t workspace(const sdm_scan_shape& S, const ScanPlan& L, char* base, ScanGates* R, ScanWs* W) {
+  const size_t units = (size_t)S.B * S.H, gb = gates_bytes(units, S.T, base, R);
+  if (L.segments < 2) return gb;
+  const size_t st = align_up(units * L.segments * S.d_v * S.d_k * 4);
+  W->first = (float*)(base + gb);
+  W->decay = (double*)(base + gb + st);
+  return gb + st + align_up(units * L.segments * 8);
 }
 
 template <bool BF16, int NK>
-hipError_t launch_blocks(const ScanArgs& A, const ScanPlan& L, const ScanWs& W, hipStream_t stream) {
+hipError_t launch_blocks(const ScanArgs& A, const ScanPlan& L, const ScanGates& R, const ScanWs& W,
+                         hipStream_t stream) {
   constexpr int lds = Tiles<BF16, NK>::bytes, states_lds = Tiles<BF16, NK>::states_bytes;
   const long long units = (long long)A.B * A.H * L.pblocks;
-  hipError_t e;
+  hipError_t e = launch_scan_gates(A, block_tokens<BF16>(), R, stream);
+  if (e != hipSuccess) return e;
   if (L.segments > 1) {
     hipLaunchKernelGGL((scan_kernel<BF16, NK, true>), dim3((unsigned)(units * (L.segments - 1))), dim3(256),
-                       states_lds, stream, A, L, W);
+                       states_lds, stream, A, L, W, R);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const long long quads = (long long)A.B * A.H * A.P * A.N / 4;
@@ -482,7 +525,8 @@ hipError_t launch_blocks(const ScanArgs& A, const ScanPlan& L, const ScanWs& W, 
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((scan_kernel<BF16, NK, false>), dim3((unsigned)(units * L.segments)), dim3(256), lds, stream, A, L, W);
+  hipLaunchKernelGGL((scan_kernel<BF16, NK, false>), dim3((unsigned)(units * L.segments)), dim3(256), lds, stream, A, L, W,
+                     R);
   return hipGetLastError();
 }
 
@@ -503,23 +547,33 @@ hipError_t launch_step(const ScanArgs& A, hipStream_t stream) {
 
 }  // namespace
 
+hipError_t launch_scan_gates(const ScanArgs& A, int Q, const ScanGates& g, hipStream_t stream) {
+  const dim3 grid((unsigned)((long long)A.B * (g.stride / 64)));
+  if (grid.x == 0) return hipSuccess;
+  if (Q == 64) hipLaunchKernelGGL(scan_gates_kernel<64>, grid, dim3(256), 0, stream, A, g);
+  else hipLaunchKernelGGL(scan_gates_kernel<32>, grid, dim3(256), 0, stream, A, g);
+  return hipGetLastError();
+}
+
 size_t scan_workspace_bytes(const sdm_scan_shape& S) {
+  ScanGates R;
   ScanWs W;
-  return workspace(S, plan_of(S), nullptr, &W);
+  return workspace(S, plan_of(S), nullptr, &R, &W);
 }
 
 hipError_t launch_scan(const sdm_scan_shape& S, const ScanArgs& A, hipStream_t stream) {
   const ScanPlan L = plan_of(S);
+  ScanGates R;
   ScanWs W{};
-  workspace(S, L, (char*)A.ws, &W);
+  workspace(S, L, (char*)A.ws, &R, &W);
   const int steps = (A.N + 31) / 32;
   if (A.bf16)
-    return steps == 1   ? launch_blocks<true, 1>(A, L, W, stream)
-           : steps == 2 ? launch_blocks<true, 2>(A, L, W, stream)
-                        : launch_blocks<true, 4>(A, L, W, stream);
-  return steps == 1   ? launch_blocks<false, 1>(A, L, W, stream)
-         : steps == 2 ? launch_blocks<false, 2>(A, L, W, stream)
-                      : launch_blocks<false, 4>(A, L, W, stream);
+    return steps == 1   ? launch_blocks<true, 1>(A, L, R, W, stream)
+           : steps == 2 ? launch_blocks<true, 2>(A, L, R, W, stream)
+                        : launch_blocks<true, 4>(A, L, R, W, stream);
+  return steps == 1   ? launch_blocks<false, 1>(A, L, R, W, stream)
+         : steps == 2 ? launch_blocks<false, 2>(A, L, R, W, stream)
+                      : launch_blocks<false, 4>(A, L, R, W, stream);
 }
 
 hipError_t launch_scan_step(const ScanArgs& A, hipStream_t stream) {

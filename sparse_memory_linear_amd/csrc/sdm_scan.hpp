@@ -179,23 +179,42 @@ __device__ __forceinline__ double add_dpp(double v) {
   return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// Inclusive sum over the lanes up to this one: shifts by 1, 2, 4, 8 in the rows of 16 lanes, then the
-// last lane of row 0 to row 1 and of row 2 to row 3, then lane 31 to rows 2 and 3
-__device__ __forceinline__ double wave_prefix(double v) {
+// Inclusive sum over the lanes of a block up to this one: shifts by 1, 2, 4, 8 in the rows of 16 lanes,
+// then the last lane of row 0 to row 1 and of row 2 to row 3, then lane 31 to rows 2 and 3
+template <int Q>
+__device__ __forceinline__ double block_prefix(double v) {  // of blocks of Q lanes, 32 or 64
   v = add_dpp<0x111, 0xF>(v);
   v = add_dpp<0x112, 0xF>(v);
   v = add_dpp<0x114, 0xF>(v);
   v = add_dpp<0x118, 0xF>(v);
   v = add_dpp<0x142, 0xA>(v);
-  return add_dpp<0x143, 0xC>(v);
+  return Q == 64 ? add_dpp<0x143, 0xC>(v) : v;
 }
 
-// Lane 63's value in every lane
-__device__ __forceinline__ double last_lane(double v) {
+__device__ __forceinline__ double read_lane(double v, int lane) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
+
+// What the products take of the time steps, [B*H][blocks of 64 tokens * 64], padding as steps of 0:
+// log2 of the decay summed over the token's block (of Q tokens), the step, and the decays as float32
+// factors from the block's start to the token and from the token (times its step) to the block's end
+struct ScanGates {
+  double* l;
+  float *step, *since, *left;
+  int stride;  // tokens per row
+};
+inline size_t gates_bytes(long long units, int T, char* base, ScanGates* g) {
+  const size_t stride = ((size_t)T + 63) / 64 * 64, n = (size_t)units * stride;
+  g->stride = (int)stride;
+  g->l = (double*)base;
+  g->step = (float*)(base + n * 8);
+  g->since = g->step + n;
+  g->left = g->since + n;
+  return align_up(n * 20);
+}
+hipError_t launch_scan_gates(const ScanArgs& A, int Q, const ScanGates& g, hipStream_t stream);
 
 }  // namespace sdm

@@ -115,48 +115,65 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   const bool xin = p0 + xk < P, kin = kk < N;
   const uint32_t xoff = (uint32_t)(xj * A.ld_x + xk) * ES, boff = (uint32_t)(kj * A.ld_b + kk) * ES,
                  coff = (uint32_t)(kj * A.ld_c + kk) * ES;
+  const uint32_t xstep = (uint32_t)(XS * A.ld_x) * ES, bstep = (uint32_t)(KS * A.ld_b) * ES,
+                 cstep = (uint32_t)(KS * A.ld_c) * ES;
   uint4 rx[NX], rb[NKV], rc[NKV];
   const bool wide = p0 + kPB <= P && N == NK * 32;  // every column of the tiles is there
-  // part `part` of `parts` of a block's pieces
-  auto fetch = [&](int c, int part, int parts) {
-    const int t0 = c * Q, here = min(max(n - t0, 0), Q);
-    const long long row0 = (long long)b * A.T + t0;
-    const char* px = (const char*)A.x + (row0 * A.ld_x + h * P + p0) * ES;
-    const char* pb_ = (const char*)A.Bm + (row0 * A.ld_b + g * N) * ES;
-    const char* pc = (const char*)A.Cm + (row0 * A.ld_c + g * N) * ES;
+  // the next block's rows, on by a block after each fetch
+  const long long row0 = (long long)b * A.T + (long long)c0 * Q;
+  const char* px = (const char*)A.x + (row0 * A.ld_x + h * P + p0) * ES;
+  const char* pB = (const char*)A.Bm + (row0 * A.ld_b + g * N) * ES;
+  const char* pC = (const char*)A.Cm + (row0 * A.ld_c + g * N) * ES;
+  const long long xblock = Q * A.ld_x * ES, bblock = Q * A.ld_b * ES, cblock = Q * A.ld_c * ES;
+  auto advance = [&] {
+    px += xblock;
+    pB += bblock;
+    if (!STATES) pC += cblock;
+  };
+  // part `part` of `parts` of a block's pieces, `here` of its tokens inside the sequence
+  auto fetch = [&](int here, int part, int parts) {
+    // kept as one 32-bit offset beside a scalar base, instead of a 64-bit address of each piece in registers
+    uint32_t xo = xoff, bo = boff, co = coff;
+    asm volatile("" : "+v"(xo), "+v"(bo), "+v"(co));
     if (wide && here == Q && Q * KR % 256 == 0) {
 #pragma unroll
       for (int i = 0; i < NKV; ++i)
         if (i % parts == part) {
-          rb[i] = *(const uint4*)(pb_ + i * KS * A.ld_b * ES + boff);
-          if (!STATES) rc[i] = *(const uint4*)(pc + i * KS * A.ld_c * ES + coff);
+          rb[i] = *(const uint4*)(pB + (bo + i * bstep));
+          if (!STATES) rc[i] = *(const uint4*)(pC + (co + i * cstep));
         }
 #pragma unroll
       for (int i = 0; i < NX; ++i)
-        if (i % parts == part) rx[i] = *(const uint4*)(px + i * XS * A.ld_x * ES + xoff);
+        if (i % parts == part) rx[i] = *(const uint4*)(px + (xo + i * xstep));
     } else {
       const int xrows = xin ? here : 0, krows = kin ? here : 0;
 #pragma unroll
       for (int i = 0; i < NKV; ++i)
         if (i % parts == part) {
           const bool in = kj + i * KS < krows;
-          rb[i] = in ? *(const uint4*)(pb_ + i * KS * A.ld_b * ES + boff) : make_uint4(0u, 0u, 0u, 0u);
-          if (!STATES) rc[i] = in ? *(const uint4*)(pc + i * KS * A.ld_c * ES + coff) : make_uint4(0u, 0u, 0u, 0u);
+          rb[i] = in ? *(const uint4*)(pB + (bo + i * bstep)) : make_uint4(0u, 0u, 0u, 0u);
+          if (!STATES) rc[i] = in ? *(const uint4*)(pC + (co + i * cstep)) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
       for (int i = 0; i < NX; ++i)
         if (i % parts == part)
-          rx[i] = xj + i * XS < xrows ? *(const uint4*)(px + i * XS * A.ld_x * ES + xoff) : make_uint4(0u, 0u, 0u, 0u);
+          rx[i] = xj + i * XS < xrows ? *(const uint4*)(px + (xo + i * xstep)) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
   // the block's gates, one token per lane
   double rl = 0.0;
   float rstep = 0.f, rfac = 0.f;
-  auto fetch_gates = [&](int c) {
-    const long long at = bh * R.stride + c * Q + (lane & (Q - 1));
-    rl = R.l[at];
-    if (!STATES) rstep = R.step[at];
-    rfac = (wave == 2 ? R.since : R.left)[at];
+  const long long gate0 = bh * R.stride + (long long)c0 * Q;
+  const double* gl = R.l + gate0;
+  const float *gstep = R.step + gate0, *gfac = (wave == 2 ? R.since : R.left) + gate0;
+  auto fetch_gates = [&] {
+    const int at = lane & (Q - 1);
+    rl = gl[at];
+    if (!STATES) rstep = gstep[at];
+    rfac = gfac[at];
+    gl += Q;
+    gstep += Q;
+    gfac += Q;
   };
   auto put_gates = [&] {
     if (lane < Q) {
@@ -188,15 +205,13 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
       for (int k = 0; k < 3; ++k) *(uint2*)(tile + k * plane + at) = make_uint2(a[k], d[k]);
     }
   };
-  // does a piece hold an infinity or a NaN?
-  auto odd = [&](const uint4& v) {
+  // the largest exponents of a piece's values, by halves (bf16) or in the high half: 0x7F80 and more in
+  // infinities and NaNs
+  auto exponents = [&](u16x2_t m, const uint4& v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool r = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r |= BF16 ? (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u
-                : (w[i] & 0x7F800000u) == 0x7F800000u;
-    return r;
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, w[i] & 0x7FFF7FFFu));
+    return m;
   };
 
   // state: tiles of 16 d_k x 16 channels, in pairs over 32 d_k: this lane holds channel p0 + 16 wave + lr,
@@ -218,11 +233,12 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   if (!STATES)  // the tiles of M right of the diagonal stay 0
     for (int i = tid; i < 3 * nM / 8; i += 256) ((uint4*)Ms)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (tid == 0) bad_[c0 & 1] = 0;
-  if (c0 < c1) fetch_gates(c0);
-  fetch(c0, 0, 1);
-  for (int c = c0; c < c1; ++c) {
-    const int t0 = c * Q, here = min(max(n - t0, 0), Q), rows = min(A.T - t0, Q);
-    float* orow = STATES ? nullptr : A.o + (bh * A.T + t0) * P + p0;
+  if (c0 < c1) fetch_gates();
+  fetch(min(max(n - c0 * Q, 0), Q), 0, 1);
+  advance();
+  float* orow = STATES ? nullptr : A.o + (bh * A.T + (long long)c0 * Q) * P + p0;
+  for (int c = c0; c < c1; ++c, orow += Q * P) {
+    const int left = n - c * Q, here = min(max(left, 0), Q), next = min(max(left - Q, 0), Q), rows = min(A.T - c * Q, Q);
     if (here == 0) {  // behind the sequence's end, like every block after it
       if (!STATES)
         for (int i = tid; i < rows * (kPB / 4); i += 256) {
@@ -232,11 +248,11 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
       continue;
     }
     __syncthreads();  // the tiles of the block before are read
-    bool weird = false;
+    u16x2_t most = {0, 0};
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       put(Xs, nX, (xj + i * XS) * LX + xk, rx[i]);
-      weird |= odd(rx[i]);
+      if (!STATES) most = exponents(most, rx[i]);
     }
 #pragma unroll
     for (int i = 0; i < NKV; ++i) {
@@ -244,12 +260,15 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
       put(Bs, nB, (kj + i * KS) * LB + kk, rb[i]);
       if (!STATES) put(Cs, nC, (kj + i * KS) * LC + kk, rc[i]);
     }
-    if (!STATES && weird) bad_[c & 1] = 1;
+    if (!STATES && (most[1] >= 0x7F80 || (BF16 && most[0] >= 0x7F80))) bad_[c & 1] = 1;
     put_gates();
     const double end = read_lane(rl, Q - 1);
     total += end;
-    if (c + 1 < c1) fetch_gates(c + 1);
-    if (STATES && c + 1 < c1) fetch(c + 1, 0, 1);
+    if (c + 1 < c1) fetch_gates();
+    if (STATES) {
+      if (c + 1 < c1) fetch(next, 0, 1);
+      advance();
+    }
     __syncthreads();
     // x of this wave's channels, tokens along k; and weighted for the state at the block's end
     const float keep = exp2_of(end);
@@ -353,28 +372,28 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
         if (k + 1 < NK) load_c(k + 1);
-        if (c + 1 < c1) fetch(c + 1, k, NK);
+        if (c + 1 < c1) fetch(next, k, NK);
         stage();
         if (k + 1 < NK) split_s(k + 1);
         mma_rows<QT>(Y, Sf[k & 1], cf[k & 1]);
         interleave<QT * 3 * (NP == 1 ? 1 : 2), NP == 1 ? 5 : 3>();
         stage();
       }
+      advance();
 #pragma unroll
       for (int it = 0; it < QT; ++it) Y[it] *= since_[16 * it + lr];
       if (!bad) {
+        load_x();
 #pragma unroll
-        for (int k = 0; k < Q / 32; ++k) {  // token tiles from 2 k on
-          Frag<3> mf[QT];
-          if (k == 0) load_x();
-#pragma unroll
-          for (int it = 2 * k; it < QT; ++it) mf[it] = along<3>(Ms + 16 * it * LM + 32 * k, LM, nM, lane);
-          stage();
+        for (int k = 0; k < Q / 32; ++k) {
           weigh_x(k);
-          if (k == 0) mma_rows<QT>(Y, xf[k], mf);
-          else mma_rows<QT - 2>(Y + 2, xf[k], mf + 2);
-          interleave<(QT - 2) * 3, 10>();
-          stage();
+#pragma unroll
+          for (int it = 2 * k; it < QT; it += 2) {  // two token tiles at a time, from the block of 32 columns on
+            Frag<3> mf[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) mf[r] = along<3>(Ms + 16 * (it + r) * LM + 32 * k, LM, nM, lane);
+            mma_rows<2>(Y + it, xf[k], mf);
+          }
         }
       } else {  // an infinity or a NaN times the zeros of M would reach earlier tokens: only j <= i
         load_x();

@@ -491,7 +491,7 @@ sdm_status sdm_selective_scan_step(const sdm_scan_shape* shape, const void* x, c
 
 /* Bytes of device memory sdm_selective_scan_backward needs as workspace: the states and their
  * gradients at every 64th token, per-head sums, and partial gradients of Bm and Cm. 0 if the
- * shape is invalid. */
+ * shape is invalid, or too large for the gradient: B * (T / 32 + 1) * H <= 2^22. */
 size_t sdm_selective_scan_backward_workspace_bytes(const sdm_scan_shape* shape);
 
 /* Gradients of L = sum <go, o> + <ds_out, s_out>. With U the gradient of the state after

@@ -20,7 +20,8 @@ LIB = os.path.join(HERE, "libsdm.so")
 ARCH = "gfx950"
 
 SOURCES = ["sdm_api.cpp", "sdm_table.hip", "sdm_address.hip", "sdm_decode.hip", "sdm_dataflow.hip", "sdm_decay.hip", "sdm_epilogue.hip", "sdm_backward.hip", "sdm_chunked.hip",
-           "sdm_api_block.cpp", "sdm_conv.hip", "sdm_scan.hip", "sdm_scan_backward.hip", "sdm_norm.hip"]
+           "sdm_api_block.cpp", "sdm_conv.hip", "sdm_scan.hip", "sdm_scan_states.hip",
+           "sdm_scan_backward.hip", "sdm_norm.hip"]
 
 CFLAGS = [
     f"--offload-arch={ARCH}",

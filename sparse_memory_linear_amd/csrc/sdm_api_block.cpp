@@ -93,6 +93,13 @@ sdm_status check_scan(const sdm_scan_shape* S) {
   return SDM_OK;
 }
 
+// The gradient's grids: one workgroup per block of 32 tokens and head at most
+sdm_status check_scan_backward(const sdm_scan_shape* S) {
+  const sdm_status st = check_scan(S);
+  if (st != SDM_OK) return st;
+  return (int64_t)S->B * (S->T / 32 + 1) * S->H > (1 << 22) ? SDM_ERR_UNSUPPORTED : SDM_OK;
+}
+
 sdm_status check_norm(const sdm_norm_shape* S) {
   if (!S) return SDM_ERR_INVALID_ARG;
   if (S->M < 0 || S->D < 1 || S->gate_rows < 0) return SDM_ERR_INVALID_ARG;
@@ -321,7 +328,7 @@ sdm_status sdm_selective_scan_step(const sdm_scan_shape* S, const void* x, const
 }
 
 size_t sdm_selective_scan_backward_workspace_bytes(const sdm_scan_shape* S) {
-  return check_scan(S) == SDM_OK ? scan_backward_workspace_bytes(*S) : 0;
+  return check_scan_backward(S) == SDM_OK ? scan_backward_workspace_bytes(*S) : 0;
 }
 
 sdm_status sdm_selective_scan_backward(const sdm_scan_shape* S, const void* x, const void* Bm, const void* Cm,
@@ -329,7 +336,7 @@ sdm_status sdm_selective_scan_backward(const sdm_scan_shape* S, const void* x, c
                                        const int32_t* lengths, const float* s_in, const float* go, const float* ds_out,
                                        float* dx, float* dBm, float* dCm, float* ddt, float* dA_log, float* ddt_bias,
                                        float* dD, float* ds_in, void* ws, size_t ws_bytes, void* stream) {
-  sdm_status st = check_scan(S);
+  sdm_status st = check_scan_backward(S);
   if (st != SDM_OK) return st;
   if ((D != nullptr) != (dD != nullptr)) return SDM_ERR_INVALID_ARG;
   const size_t need = scan_backward_workspace_bytes(*S);

@@ -35,50 +35,20 @@ struct ScanWs {
   double* decay;  // [segments][B*H]: log2 of the segments' decay
 };
 
-// LDS of one workgroup: tiles of B, C, x (NP planes each) and M (3 planes). Row strides keep the 8-byte
+// LDS of one workgroup: tiles of B, x, C (NP planes each) and M (3 planes). Row strides keep the 8-byte
 // reads along rows and the transposing reads over 16 rows on different banks.
 template <bool BF16, int NK>
 struct Tiles {
   static constexpr int Q = block_tokens<BF16>(), NP = BF16 ? 1 : 3;
   static constexpr int LB = NK * 32 + 16, LC = NK * 32 + 8, LX = kPB + 16, LM = Q + 8;
   static constexpr int nB = Q * LB, nC = Q * LC, nX = Q * LX, nM = Q * LM;
-  static constexpr int bytes = (NP * (nB + nX + nC) + 3 * nM) * 2, states_bytes = NP * (nB + nX) * 2;
+  static constexpr int bytes = (NP * (nB + nX + nC) + 3 * nM) * 2;
 };
-
-// ------------------------------------------------------------------ time steps
-// A workgroup takes 64 tokens of a sequence, all heads: dt comes in along the heads, goes through LDS and
-// is summed along the tokens, one per lane.
-template <int Q>
-__global__ void __launch_bounds__(256) scan_gates_kernel(ScanArgs A, ScanGates g) {
-  __shared__ float tile[64][65];
-  const int blocks = g.stride / 64, b = blockIdx.x / blocks, t0 = (int)(blockIdx.x % blocks) * 64;
-  const int here = min(max(sequence_length(A.lengths, b, A.T) - t0, 0), 64);
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int h0 = 0; h0 < A.H; h0 += 64) {
-    const int heads = min(A.H - h0, 64);
-    __syncthreads();
-    for (int i = threadIdx.x; i < here * heads; i += 256)
-      tile[i / heads][i % heads] = A.dt[((long long)b * A.T + t0 + i / heads) * A.ld_dt + h0 + i % heads];
-    __syncthreads();
-    for (int h = wave; h < heads; h += 4) {
-      const float step = lane < here ? softplus(tile[lane][h] + A.dt_bias[h0 + h]) : 0.f;
-      const float la = lane < here ? fmaxf(-expf(A.A_log[h0 + h]) * step, -kMaxDecay) : 0.f;
-      const double l = block_prefix<Q>((double)la * kLog2e);
-      const double end = Q == 64 || lane >= 32 ? read_lane(l, 63) : read_lane(l, 31);
-      const long long at = ((long long)b * A.H + h0 + h) * g.stride + t0 + lane;
-      g.l[at] = l;
-      g.step[at] = step;
-      g.since[at] = exp2_of(l);
-      g.left[at] = exp2_of(end - l) * step;
-    }
-  }
-}
 
 // ------------------------------------------------------------------ prompts
 // One workgroup walks the blocks of a segment of a (sequence, head, 64 channels) unit with the state in
 // the accumulators of its matrix products: wave w holds channels 16 w .. 16 w + 15, all d_k.
-// STATES: only the state at the segment's end is wanted (of all segments but the last).
-template <bool BF16, int NK, bool STATES>
+template <bool BF16, int NK>
 __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, ScanWs W, ScanGates R) {
   using TL = Tiles<BF16, NK>;
   constexpr int Q = TL::Q, NP = TL::NP, NT = 2 * NK, QT = Q / 16;
@@ -94,7 +64,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   // unit: the heads of a group side by side on one XCD (workgroups go to the 8 XCDs in turn), so that its
   // L2 holds the B and C they share
   const int hpg = A.H / A.G;
-  const int fast = A.B * A.G * (STATES ? L.segments - 1 : L.segments);
+  const int fast = A.B * A.G * L.segments;
   const int f = blockIdx.x % fast, s = blockIdx.x / fast;
   const int seg = f / (A.B * A.G), bg = f % (A.B * A.G), b = bg / A.G, g = bg % A.G;
   const int h = g * hpg + s % hpg, pb = s / hpg;
@@ -128,7 +98,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   auto advance = [&] {
     px += xblock;
     pB += bblock;
-    if (!STATES) pC += cblock;
+    pC += cblock;
   };
   // part `part` of `parts` of a block's pieces, `here` of its tokens inside the sequence
   auto fetch = [&](int here, int part, int parts) {
@@ -140,7 +110,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
       for (int i = 0; i < NKV; ++i)
         if (i % parts == part) {
           rb[i] = *(const uint4*)(pB + (bo + i * bstep));
-          if (!STATES) rc[i] = *(const uint4*)(pC + (co + i * cstep));
+          rc[i] = *(const uint4*)(pC + (co + i * cstep));
         }
 #pragma unroll
       for (int i = 0; i < NX; ++i)
@@ -152,7 +122,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
         if (i % parts == part) {
           const bool in = kj + i * KS < krows;
           rb[i] = in ? *(const uint4*)(pB + (bo + i * bstep)) : make_uint4(0u, 0u, 0u, 0u);
-          if (!STATES) rc[i] = in ? *(const uint4*)(pC + (co + i * cstep)) : make_uint4(0u, 0u, 0u, 0u);
+          rc[i] = in ? *(const uint4*)(pC + (co + i * cstep)) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
       for (int i = 0; i < NX; ++i)
@@ -169,7 +139,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   auto fetch_gates = [&] {
     const int at = lane & (Q - 1);
     rl = gl[at];
-    if (!STATES) rstep = gstep[at];
+    rstep = gstep[at];
     rfac = gfac[at];
     gl += Q;
     gstep += Q;
@@ -178,12 +148,10 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   auto put_gates = [&] {
     if (lane < Q) {
       if (wave == 3) left_[lane] = rfac;
-      if (STATES) return;
       if (wave == 0) l_[lane] = rl;
       if (wave == 1) step_[lane] = rstep;
       if (wave == 2) since_[lane] = rfac;
     }
-    if (STATES) return;
     double from = 0.0;  // log-decay at the start of this lane's tile
 #pragma unroll
     for (int it = 1; it < QT; ++it) {
@@ -221,26 +189,24 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   const long long srow = (bh * P + p) * N;
   f32x4_t S[NT];
   {
-    const float* from = STATES ? nullptr : L.segments > 1 ? W.first + (long long)seg * A.B * A.H * P * N : A.s_in;
+    const float* from = L.segments > 1 ? W.first + (long long)seg * A.B * A.H * P * N : A.s_in;
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
       const int k = state_at(m);
       S[m] = from && p < P && k < N ? *(const f32x4_t*)(from + srow + k) : f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
   }
-  double total = 0.0;  // log2 of the decay since the segment's start
 
-  if (!STATES)  // the tiles of M right of the diagonal stay 0
-    for (int i = tid; i < 3 * nM / 8; i += 256) ((uint4*)Ms)[i] = make_uint4(0u, 0u, 0u, 0u);
+  // the tiles of M right of the diagonal stay 0
+  for (int i = tid; i < 3 * nM / 8; i += 256) ((uint4*)Ms)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (tid == 0) bad_[c0 & 1] = 0;
   if (c0 < c1) fetch_gates();
   fetch(min(max(n - c0 * Q, 0), Q), 0, 1);
   advance();
-  float* orow = STATES ? nullptr : A.o + (bh * A.T + (long long)c0 * Q) * P + p0;
+  float* orow = A.o + (bh * A.T + (long long)c0 * Q) * P + p0;
   for (int c = c0; c < c1; ++c, orow += Q * P) {
     const int left = n - c * Q, here = min(max(left, 0), Q), next = min(max(left - Q, 0), Q), rows = min(A.T - c * Q, Q);
     if (here == 0) {  // behind the sequence's end, like every block after it
-      if (!STATES)
         for (int i = tid; i < rows * (kPB / 4); i += 256) {
           const int k = (i % (kPB / 4)) * 4;
           if (p0 + k < P) *(float4*)(orow + (long long)(i / (kPB / 4)) * P + k) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -252,23 +218,18 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       put(Xs, nX, (xj + i * XS) * LX + xk, rx[i]);
-      if (!STATES) most = exponents(most, rx[i]);
+      most = exponents(most, rx[i]);
     }
 #pragma unroll
     for (int i = 0; i < NKV; ++i) {
       if (Q * KR % 256 != 0 && kj + i * KS >= Q) continue;
       put(Bs, nB, (kj + i * KS) * LB + kk, rb[i]);
-      if (!STATES) put(Cs, nC, (kj + i * KS) * LC + kk, rc[i]);
+      put(Cs, nC, (kj + i * KS) * LC + kk, rc[i]);
     }
-    if (!STATES && (most[1] >= 0x7F80 || (BF16 && most[0] >= 0x7F80))) bad_[c & 1] = 1;
+    if ((most[1] >= 0x7F80 || (BF16 && most[0] >= 0x7F80))) bad_[c & 1] = 1;
     put_gates();
     const double end = read_lane(rl, Q - 1);
-    total += end;
     if (c + 1 < c1) fetch_gates();
-    if (STATES) {
-      if (c + 1 < c1) fetch(next, 0, 1);
-      advance();
-    }
     __syncthreads();
     // x of this wave's channels, tokens along k; and weighted for the state at the block's end
     const float keep = exp2_of(end);
@@ -288,150 +249,141 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
       xw[k] = split8(v);
     };
 
-    if (!STATES) {
-      if (tid == 0) bad_[(c + 1) & 1] = 0;
-      // M, tiles (it, jt) in turn over the waves, those on the diagonal first; a wave without one more
-      // repeats the last
-      constexpr int MT = QT * (QT + 1) / 2, MW = (MT + 3) / 4;
-      f32x4_t G[MW];
-      int it_[MW], jt_[MW];
+    if (tid == 0) bad_[(c + 1) & 1] = 0;
+    // M, tiles (it, jt) in turn over the waves, those on the diagonal first; a wave without one more
+    // repeats the last
+    constexpr int MT = QT * (QT + 1) / 2, MW = (MT + 3) / 4;
+    f32x4_t G[MW];
+    int it_[MW], jt_[MW];
 #pragma unroll
-      for (int e = 0; e < MW; ++e) {
-        const int t = min(wave + 4 * e, MT - 1);
-        int it = 1, jt = t - QT;
-        while (jt >= it) jt -= it++;
-        it_[e] = t < QT ? t : it;
-        jt_[e] = t < QT ? t : jt;
-        G[e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      }
-      Frag<NP> gb[2][MW], gc[2][MW];
-      auto load_g = [&](int k) {
-#pragma unroll
-        for (int e = 0; e < MW; ++e) {
-          gb[k & 1][e] = along<NP>(Bs + 16 * jt_[e] * LB + 32 * k, LB, nB, lane);
-          gc[k & 1][e] = along<NP>(Cs + 16 * it_[e] * LC + 32 * k, LC, nC, lane);
-        }
-      };
-      load_g(0);
-#pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        if (k + 1 < NK) load_g(k + 1);
-        stage();
-#pragma unroll
-        for (int e = 0; e < MW; ++e) mma(G[e], gb[k & 1][e], gc[k & 1][e]);
-      }
-#pragma unroll
-      for (int e = 0; e < MW; ++e) {
-        const int i = 16 * it_[e] + lr, j = 16 * jt_[e] + 4 * lg;
-        float mv[4];
-        if (it_[e] != jt_[e]) {
-          const float up = up_[i];
-          const f32x4_t down = *(const f32x4_t*)(down_[it_[e]] + j);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) mv[u] = G[e][u] * (up * down[u]);
-        } else {
-          const double li = l_[i];
-          const double2 l0 = *(const double2*)(l_ + j), l1 = *(const double2*)(l_ + j + 2);
-          const f32x4_t step = *(const f32x4_t*)(step_ + j);
-          const double lj[4] = {l0.x, l0.y, l1.x, l1.y};
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            // right of the diagonal whatever the product is gives 0, by its bits: no branch around the exp
-            const float v = G[e][u] * (exp2_of(li - lj[u]) * step[u]);
-            mv[u] = __uint_as_float(__float_as_uint(v) & (j + u <= i ? ~0u : 0u)) +
-                    __uint_as_float(__float_as_uint(D) & (j + u == i ? ~0u : 0u));
-          }
-        }
-        uint32_t w0[3], w1[3];
-        split_pair(mv[0], mv[1], w0);
-        split_pair(mv[2], mv[3], w1);
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-          *(uint2*)(Ms + k * nM + i * LM + across_order(j)) = make_uint2(w0[k], w1[k]);
-      }
-      f32x4_t Y[QT];
-      Frag<NP> cf[2][QT];
-      auto load_c = [&](int k) {
-#pragma unroll
-        for (int it = 0; it < QT; ++it) cf[k & 1][it] = along<NP>(Cs + 16 * it * LC + 32 * k, LC, nC, lane);
-      };
-      load_c(0);
-#pragma unroll
-      for (int it = 0; it < QT; ++it) Y[it] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      Frag<3> Sf[2];
-      auto split_s = [&](int k) {  // the pieces of 32 d_k of the state, which then decays to the block's end
-        const float v[8] = {S[2 * k][0], S[2 * k][1], S[2 * k][2], S[2 * k][3],
-                            S[2 * k + 1][0], S[2 * k + 1][1], S[2 * k + 1][2], S[2 * k + 1][3]};
-        Sf[k & 1] = split8(v);
-        S[2 * k] *= keep;
-        S[2 * k + 1] *= keep;
-      };
-      split_s(0);
-      __syncthreads();
-      const bool bad = bad_[c & 1] != 0;
-#pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        if (k + 1 < NK) load_c(k + 1);
-        if (c + 1 < c1) fetch(next, k, NK);
-        stage();
-        if (k + 1 < NK) split_s(k + 1);
-        mma_rows<QT>(Y, Sf[k & 1], cf[k & 1]);
-        interleave<QT * 3 * (NP == 1 ? 1 : 2), NP == 1 ? 5 : 3>();
-        stage();
-      }
-      advance();
-#pragma unroll
-      for (int it = 0; it < QT; ++it) Y[it] *= since_[16 * it + lr];
-      if (!bad) {
-        load_x();
-#pragma unroll
-        for (int k = 0; k < Q / 32; ++k) {
-          weigh_x(k);
-#pragma unroll
-          for (int it = 2 * k; it < QT; it += 2) {  // two token tiles at a time, from the block of 32 columns on
-            Frag<3> mf[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) mf[r] = along<3>(Ms + 16 * (it + r) * LM + 32 * k, LM, nM, lane);
-            mma_rows<2>(Y + it, xf[k], mf);
-          }
-        }
-      } else {  // an infinity or a NaN times the zeros of M would reach earlier tokens: only j <= i
-        load_x();
-#pragma unroll
-        for (int k = 0; k < Q / 32; ++k) weigh_x(k);
-#pragma unroll
-        for (int it = 0; it < QT; ++it)
-          for (int j = 0; j <= 16 * it + lr; ++j) {
-            const uint16_t* mp = Ms + (16 * it + lr) * LM + across_order(j);
-            const float m = bf16_to_f32(mp[0]) + bf16_to_f32(mp[nM]) + bf16_to_f32(mp[2 * nM]);
-            for (int k = NP - 1; k >= 0; --k) {
-              const uint2 q = *(const uint2*)(Xs + k * nX + j * LX + 16 * wave + 4 * lg);
-              Y[it][0] = fmaf(m, bf16lo(q.x), Y[it][0]);
-              Y[it][1] = fmaf(m, bf16hi(q.x), Y[it][1]);
-              Y[it][2] = fmaf(m, bf16lo(q.y), Y[it][2]);
-              Y[it][3] = fmaf(m, bf16hi(q.y), Y[it][3]);
-            }
-          }
-      }
-      float* oo = orow + (long long)lr * P + 16 * wave + 4 * lg;
-      if (wide && here == Q) {
-#pragma unroll
-        for (int it = 0; it < QT; ++it) *(f32x4_t*)(oo + 16 * it * P) = Y[it];
-      } else if (p0 + 16 * wave + 4 * lg < P) {
-#pragma unroll
-        for (int it = 0; it < QT; ++it)
-          if (16 * it + lr < rows)
-            *(f32x4_t*)(oo + 16 * it * P) = 16 * it + lr < here ? Y[it] : f32x4_t{0.f, 0.f, 0.f, 0.f};
-      }
+    for (int e = 0; e < MW; ++e) {
+      const int t = min(wave + 4 * e, MT - 1);
+      int it = 1, jt = t - QT;
+      while (jt >= it) jt -= it++;
+      it_[e] = t < QT ? t : it;
+      jt_[e] = t < QT ? t : jt;
+      G[e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-    // the state at the block's end
-    if (STATES) {
+    Frag<NP> gb[2][MW], gc[2][MW];
+    auto load_g = [&](int k) {
+#pragma unroll
+      for (int e = 0; e < MW; ++e) {
+        gb[k & 1][e] = along<NP>(Bs + 16 * jt_[e] * LB + 32 * k, LB, nB, lane);
+        gc[k & 1][e] = along<NP>(Cs + 16 * it_[e] * LC + 32 * k, LC, nC, lane);
+      }
+    };
+    load_g(0);
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      if (k + 1 < NK) load_g(k + 1);
+      stage();
+#pragma unroll
+      for (int e = 0; e < MW; ++e) mma(G[e], gb[k & 1][e], gc[k & 1][e]);
+    }
+#pragma unroll
+    for (int e = 0; e < MW; ++e) {
+      const int i = 16 * it_[e] + lr, j = 16 * jt_[e] + 4 * lg;
+      float mv[4];
+      if (it_[e] != jt_[e]) {
+        const float up = up_[i];
+        const f32x4_t down = *(const f32x4_t*)(down_[it_[e]] + j);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mv[u] = G[e][u] * (up * down[u]);
+      } else {
+        const double li = l_[i];
+        const double2 l0 = *(const double2*)(l_ + j), l1 = *(const double2*)(l_ + j + 2);
+        const f32x4_t step = *(const f32x4_t*)(step_ + j);
+        const double lj[4] = {l0.x, l0.y, l1.x, l1.y};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          // right of the diagonal whatever the product is gives 0, by its bits: no branch around the exp
+          const float v = G[e][u] * (exp2_of(li - lj[u]) * step[u]);
+          mv[u] = __uint_as_float(__float_as_uint(v) & (j + u <= i ? ~0u : 0u)) +
+                  __uint_as_float(__float_as_uint(D) & (j + u == i ? ~0u : 0u));
+        }
+      }
+      uint32_t w0[3], w1[3];
+      split_pair(mv[0], mv[1], w0);
+      split_pair(mv[2], mv[3], w1);
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *(uint2*)(Ms + k * nM + i * LM + across_order(j)) = make_uint2(w0[k], w1[k]);
+    }
+    f32x4_t Y[QT];
+    Frag<NP> cf[2][QT];
+    auto load_c = [&](int k) {
+#pragma unroll
+      for (int it = 0; it < QT; ++it) cf[k & 1][it] = along<NP>(Cs + 16 * it * LC + 32 * k, LC, nC, lane);
+    };
+    load_c(0);
+#pragma unroll
+    for (int it = 0; it < QT; ++it) Y[it] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    Frag<3> Sf[2];
+    auto split_s = [&](int k) {  // the pieces of 32 d_k of the state, which then decays to the block's end
+      const float v[8] = {S[2 * k][0], S[2 * k][1], S[2 * k][2], S[2 * k][3],
+                          S[2 * k + 1][0], S[2 * k + 1][1], S[2 * k + 1][2], S[2 * k + 1][3]};
+      Sf[k & 1] = split8(v);
+      S[2 * k] *= keep;
+      S[2 * k + 1] *= keep;
+    };
+    split_s(0);
+    __syncthreads();
+    const bool bad = bad_[c & 1] != 0;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      if (k + 1 < NK) load_c(k + 1);
+      if (c + 1 < c1) fetch(next, k, NK);
+      stage();
+      if (k + 1 < NK) split_s(k + 1);
+      mma_rows<QT>(Y, Sf[k & 1], cf[k & 1]);
+      interleave<QT * 3 * (NP == 1 ? 1 : 2), NP == 1 ? 5 : 3>();
+      stage();
+    }
+    advance();
+#pragma unroll
+    for (int it = 0; it < QT; ++it) Y[it] *= since_[16 * it + lr];
+    if (!bad) {
+      load_x();
+#pragma unroll
+      for (int k = 0; k < Q / 32; ++k) {
+        weigh_x(k);
+#pragma unroll
+        for (int it = 2 * k; it < QT; it += 2) {  // two token tiles at a time, from the block of 32 columns on
+          Frag<3> mf[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) mf[r] = along<3>(Ms + 16 * (it + r) * LM + 32 * k, LM, nM, lane);
+          mma_rows<2>(Y + it, xf[k], mf);
+        }
+      }
+    } else {  // an infinity or a NaN times the zeros of M would reach earlier tokens: only j <= i
       load_x();
 #pragma unroll
       for (int k = 0; k < Q / 32; ++k) weigh_x(k);
 #pragma unroll
-      for (int m = 0; m < NT; ++m) S[m] *= keep;
+      for (int it = 0; it < QT; ++it)
+        for (int j = 0; j <= 16 * it + lr; ++j) {
+          const uint16_t* mp = Ms + (16 * it + lr) * LM + across_order(j);
+          const float m = bf16_to_f32(mp[0]) + bf16_to_f32(mp[nM]) + bf16_to_f32(mp[2 * nM]);
+          for (int k = NP - 1; k >= 0; --k) {
+            const uint2 q = *(const uint2*)(Xs + k * nX + j * LX + 16 * wave + 4 * lg);
+            Y[it][0] = fmaf(m, bf16lo(q.x), Y[it][0]);
+            Y[it][1] = fmaf(m, bf16hi(q.x), Y[it][1]);
+            Y[it][2] = fmaf(m, bf16lo(q.y), Y[it][2]);
+            Y[it][3] = fmaf(m, bf16hi(q.y), Y[it][3]);
+          }
+        }
     }
+    float* oo = orow + (long long)lr * P + 16 * wave + 4 * lg;
+    if (wide && here == Q) {
+#pragma unroll
+      for (int it = 0; it < QT; ++it) *(f32x4_t*)(oo + 16 * it * P) = Y[it];
+    } else if (p0 + 16 * wave + 4 * lg < P) {
+#pragma unroll
+      for (int it = 0; it < QT; ++it)
+        if (16 * it + lr < rows)
+          *(f32x4_t*)(oo + 16 * it * P) = 16 * it + lr < here ? Y[it] : f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    // the state at the block's end
     constexpr int MH = NT < 4 ? NT : 4;  // tiles of d_k at a time
     Frag<NP> bf[2][MH];
     auto load_b = [&](int s) {  // step s: 32 tokens, MH tiles
@@ -448,29 +400,13 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
       mma_cols<MH>(S + s % (NT / MH) * MH, bf[s & 1], xw[s / (NT / MH)]);
     }
   }
-  float* to = STATES ? W.first + (long long)(seg + 1) * A.B * A.H * P * N : seg + 1 == L.segments ? A.s_out : nullptr;
+  float* to = seg + 1 == L.segments ? A.s_out : nullptr;
   if (to && p < P) {
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
       const int k = state_at(m);
       if (k < N) *(f32x4_t*)(to + srow + k) = S[m];
     }
-  }
-  if (STATES && tid == 0 && pb == 0) W.decay[(long long)(seg + 1) * A.B * A.H + bh] = total;
-}
-
-// States before the segments, from the segments' own ends: first[0] is the call's first state, first[s]
-// (which holds what segment s-1 adds) takes up first[s-1] decayed over segment s-1.
-__global__ void __launch_bounds__(256) scan_join_kernel(ScanArgs A, ScanPlan L, ScanWs W) {
-  const long long per = (long long)A.P * A.N / 4, units = (long long)A.B * A.H;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= units * per) return;
-  f32x4_t* v = (f32x4_t*)W.first;
-  f32x4_t s = A.s_in ? ((const f32x4_t*)A.s_in)[i] : f32x4_t{0.f, 0.f, 0.f, 0.f};
-  v[i] = s;
-  for (int k = 1; k < L.segments; ++k) {
-    s = v[k * units * per + i] + s * exp2_of(W.decay[k * units + i / per]);
-    v[k * units * per + i] = s;
   }
 }
 
@@ -504,17 +440,13 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs A) {
   if (live && k == 0) A.o[(long long)bh * A.P + p] = fmaf(A.D ? A.D[h] : 0.f, x, o);
 }
 
-// A call of few units is split into token segments until about two workgroups per compute unit are
-// busy, each of at least four blocks: the pass over x and B that a split costs is then shared by enough.
 ScanPlan plan_of(const sdm_scan_shape& S) {
   const int Q = S.in_dtype == SDM_BF16 ? block_tokens<true>() : block_tokens<false>();
   ScanPlan L;
   L.pblocks = (S.d_v + kPB - 1) / kPB;
   L.blocks = (S.T + Q - 1) / Q;
   const long long units = (long long)S.B * S.H * L.pblocks;
-  long long s = 512 / units;
-  if (s > L.blocks / 4) s = L.blocks / 4;
-  L.segments = s < 1 ? 1 : (int)s;
+  L.segments = scan_segments(units, L.blocks, 512);  // two workgroups per compute unit
   return L;
 }
 
@@ -530,22 +462,37 @@ size_t workspace(const sdm_scan_shape& S, const ScanPlan& L, char* base, ScanGat
 template <bool BF16, int NK>
 hipError_t launch_blocks(const ScanArgs& A, const ScanPlan& L, const ScanGates& R, const ScanWs& W,
                          hipStream_t stream) {
-  constexpr int lds = Tiles<BF16, NK>::bytes, states_lds = Tiles<BF16, NK>::states_bytes;
-  const long long units = (long long)A.B * A.H * L.pblocks;
   hipError_t e = launch_scan_gates(A, block_tokens<BF16>(), R, stream);
   if (e != hipSuccess) return e;
   if (L.segments > 1) {
-    hipLaunchKernelGGL((scan_kernel<BF16, NK, true>), dim3((unsigned)(units * (L.segments - 1))), dim3(256),
-                       states_lds, stream, A, L, W, R);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const long long quads = (long long)A.B * A.H * A.P * A.N / 4;
-    hipLaunchKernelGGL(scan_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, A, L, W);
-    e = hipGetLastError();
+    ScanWalk K{};
+    K.B = A.B;
+    K.T = A.T;
+    K.H = A.H;
+    K.G = A.G;
+    K.N = A.N;
+    K.P = A.P;
+    K.blocks = L.blocks;
+    K.segments = L.segments;
+    K.stride = R.stride;
+    K.X = A.x;
+    K.K = A.Bm;
+    K.xb = (long long)A.T * A.ld_x;
+    K.xh = A.P;
+    K.ld_x = A.ld_x;
+    K.ld_k = A.ld_b;
+    K.lengths = A.lengths;
+    K.weight = R.left;
+    K.l = R.l;
+    K.start = A.s_in;
+    K.first = W.first;
+    K.decay = W.decay;
+    e = launch_scan_walk(K, BF16, false, stream);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((scan_kernel<BF16, NK, false>), dim3((unsigned)(units * L.segments)), dim3(256), lds, stream, A, L, W,
-                     R);
+  constexpr int lds = Tiles<BF16, NK>::bytes;
+  const long long units = (long long)A.B * A.H * L.pblocks;
+  hipLaunchKernelGGL((scan_kernel<BF16, NK>), dim3((unsigned)(units * L.segments)), dim3(256), lds, stream, A, L, W, R);
   return hipGetLastError();
 }
 
@@ -565,14 +512,6 @@ hipError_t launch_step(const ScanArgs& A, hipStream_t stream) {
 }
 
 }  // namespace
-
-hipError_t launch_scan_gates(const ScanArgs& A, int Q, const ScanGates& g, hipStream_t stream) {
-  const dim3 grid((unsigned)((long long)A.B * (g.stride / 64)));
-  if (grid.x == 0) return hipSuccess;
-  if (Q == 64) hipLaunchKernelGGL(scan_gates_kernel<64>, grid, dim3(256), 0, stream, A, g);
-  else hipLaunchKernelGGL(scan_gates_kernel<32>, grid, dim3(256), 0, stream, A, g);
-  return hipGetLastError();
-}
 
 size_t scan_workspace_bytes(const sdm_scan_shape& S) {
   ScanGates R;

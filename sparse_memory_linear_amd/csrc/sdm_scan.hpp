@@ -218,4 +218,28 @@ inline size_t gates_bytes(long long units, int T, char* base, ScanGates* g) {
 }
 hipError_t launch_scan_gates(const ScanArgs& A, int Q, const ScanGates& g, hipStream_t stream);
 
+// One walk over the blocks (sdm_scan_states.hip): token t of (b, h) has X at b xb + h xh + t ld_x, K at
+// (b T + t) ld_k + g N, its weight and log-decay at (b H + h) stride + t.
+struct ScanWalk {
+  int B, T, H, G, N, P, blocks, segments, segs, stride;
+  const void *X, *K;
+  long long xb, xh, ld_x, ld_k;
+  const int32_t* lengths;
+  const float* weight;
+  const double* l;
+  const float* start;  // state before the walk, or null
+  float* end;          // state behind it, or null
+  float* first;        // [segments][B*H][P][N]: states before the segments
+  double* decay;       // [segments][B*H]: log2 of the segments' decay
+  float* states;       // [B*H][blocks][P N] states entering the blocks, or null: only `first` is wanted
+};
+// Segments of a walk (or of the forward kernel): a call of few units is split until `wanted` workgroups are
+// busy, each with at least four blocks, so that enough share the pass that finds the segments' first states.
+inline int scan_segments(long long units, int blocks, int wanted) {
+  long long s = wanted / units;
+  if (s > blocks / 4) s = blocks / 4;
+  return s < 1 ? 1 : (int)s;
+}
+hipError_t launch_scan_walk(const ScanWalk& A, bool bf16, bool back, hipStream_t stream);
+
 }  // namespace sdm

@@ -1,16 +1,24 @@
 // Gradient of the selective scan. With U the gradient of the state after token t and e = -exp(A_log):
 //
-//   dC_t = S_t^T go_t,  dx_t = dtv U B_t + D go_t,  dB_t = dtv U^T x_t,
-//   dl_t = a_t <U, S_{t-1}>,  ddtv = x_t^T U B_t + e dl_t
+//   dC_t = S_t^T go_t,  dx_t = step U B_t + D go_t,  dB_t = step U^T x_t,
+//   dl_t = a_t <U, S_{t-1}>,  dstep_t = x_t^T U B_t + e dl_t
 //
-// in blocks of 64 tokens. With l the log-decay summed from the block's start, E_ij = exp(l_i - l_j) for
+// in blocks of Q tokens. With l the log-decay summed from the block's start, E_ij = exp(l_i - l_j) for
 // j <= i, S the state before the block, U the gradient of the state after it, w_j = exp(l_end - l_j):
-//   Gm = C B^T, Pm = go x^T
-//   dC_i = sum_j Pm_ij E_ij dtv_j B_j + exp(l_i) S^T go_i
-//   dx_j = dtv_j (sum_i Gm_ij E_ij go_i + w_j U B_j) + D go_j
-//   dB_j = dtv_j (sum_i Pm_ij E_ij C_i + w_j U^T x_j)
-//   dl_t = sum over pairs j < t <= i of F_ij (F = Pm E Gm dtv_j) + sum_{i >= t} exp(l_i) go_i.(S C_i)
-//          + sum_{j < t} w_j dtv_j x_j.(U B_j) + exp(l_end) <U, S>
+//   G = C B^T, P = go x^T,  M_ij = G_ij E_ij step_j,  R_ij = P_ij E_ij step_j
+//   dx_j = sum_i M_ij go_i + w_j step_j U B_j + D go_j
+//   dC_i = sum_j R_ij B_j + exp(l_i) S^T go_i,   dB_j = sum_i R_ij C_i + w_j step_j U^T x_j
+//   dl_t = sum over pairs j < t <= i of F_ij step_j + sum_{i >= t} read_i + sum_{j < t} step_j put_j
+//          + exp(l_end) <U, S>
+//   with F_ij = P_ij E_ij G_ij, read_i = exp(l_i) C_i . S^T go_i, put_j = w_j B_j . U^T x_j
+//   x_j^T U_j B_j = sum_{i >= j} F_ij + put_j
+// The pairs' sum over a token is a difference of sums over rows and columns of F: both are taken in
+// float64 of the same float32 F, so that what is on both sides cancels.
+//
+// Three steps: the states S of all blocks (a walk over x and B), the gradients U (a walk over go and C from
+// the end), then every block by itself. A workgroup of 8 waves takes one block of one group and some of its
+// heads, one after the other, and sums their dB and dC in registers; G is formed once. Every product runs on
+// the matrix cores with float32 factors as three bf16 pieces.
 
 #include "sdm_device.hpp"
 #include "sdm_internal.hpp"
@@ -20,219 +28,484 @@ namespace sdm {
 
 namespace {
 
-constexpr int Q = 64;  // tokens per block
+constexpr int kPB = 64;       // channels per tile
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
 
-struct ScanBwdWs {
-  float* S;      // [B,H,nb,P,N] states before the blocks
-  float* U;      // [B,H,nb,P,N] gradients of the states after them
-  double* sums;  // [B,nb,H,3] dA_log, ddt_bias, dD
-  int nb;
+struct ScanBwd {
+  const float* S;  // [B*H][blocks][N][P]
+  const float* U;  // [B*H][blocks][P][N]
+  double* sums;    // [B*blocks][H][3]: dA_log, ddt_bias, dD of the block
+  float* part;     // [parts][2][B*T][G*N]: dC and dB of the parts' heads (parts > 1)
+  int blocks, parts, heads;  // heads per part
 };
 
-int blocks_of(int T) { return (T + Q - 1) / Q; }
+template <bool BF16, int NK>
+struct BwdTiles {
+  static constexpr int Q = BF16 ? 64 : 32, NP = BF16 ? 1 : 3, QT = Q / 16, NT = 2 * NK;
+  static constexpr int LB = NK * 32 + 16, LX = kPB + 16, LM = Q + 8, LU = NK * 32 + 16;
+  static constexpr int nB = Q * LB, nX = Q * LX, nM = Q * LM, nU = kPB * LU;
+  static constexpr int shared = nU > 2 * nM ? 3 * nU : 6 * nM;  // U takes the place of M and R
+  static constexpr int bytes = (2 * NP * nB + (NP + 3) * nX + shared) * 2;
+  static constexpr int MT = QT * (QT + 1) / 2;  // tiles of M on and below the diagonal
+};
 
-__host__ __device__ inline size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
+template <bool BF16, int NK>
+__global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, ScanGates R, ScanBwd W) {
+  using TL = BwdTiles<BF16, NK>;
+  constexpr int Q = TL::Q, NP = TL::NP, QT = TL::QT, NT = TL::NT, MT = TL::MT;
+  constexpr int LB = TL::LB, LX = TL::LX, LM = TL::LM, LU = TL::LU, nB = TL::nB, nX = TL::nX, nM = TL::nM, nU = TL::nU;
+  extern __shared__ __align__(16) uint16_t lds[];
+  __shared__ __align__(16) double l_[Q], row_[MT][16], col_[MT][16], us_[kWaves];
+  __shared__ __align__(16) float step_[Q], since_[Q], left_[Q], w_[Q], up_[Q], diag_[Q], trace_[Q];
+  __shared__ __align__(16) float read_[NT][Q], put_[NT][Q];
+  uint16_t *Bs = lds, *Cs = Bs + NP * nB, *Xs = Cs + NP * nB, *Gs = Xs + NP * nX, *Ms = Gs + 3 * nX, *Rs = Ms + 3 * nM,
+           *Us = Ms;
 
-// One wave per (sequence, head, channel): dir = 0 walks the tokens forward and stores the state
-// before every block, dir = 1 backward and stores the gradient of the state after it.
-template <bool BF16>
-__global__ void __launch_bounds__(256) scan_states_kernel(ScanArgs A, ScanBwdWs W, int dir) {
-  const long long u = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (u >= (long long)A.B * A.H * A.P) return;
-  const int lane = threadIdx.x & 63;
-  const int p = (int)(u % A.P), h = (int)(u / A.P % A.H), b = (int)(u / A.P / A.H);
-  const int g = h / (A.H / A.G);
-  const int n = sequence_length(A.lengths, b, A.T);
-  const float rate = -expf(A.A_log[h]), bias = A.dt_bias[h];
-  const float* first = dir ? A.ds_out : A.s_in;
-  float* out = dir ? W.U : W.S;
-  float s[2] = {0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (first && lane + 64 * i < A.N) s[i] = first[u * A.N + lane + 64 * i];
-  for (int c = 0; c < W.nb; ++c) {
-    const int blk = dir ? W.nb - 1 - c : c;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int k = lane + 64 * i;
-      if (k < A.N) out[(((u / A.P) * W.nb + blk) * A.P + p) * A.N + k] = s[i];
+  int id = blockIdx.x;
+  const int part = id % W.parts;
+  id /= W.parts;
+  const int g = id % A.G;
+  id /= A.G;
+  const int blk = id % W.blocks, b = id / W.blocks;
+  const int hpg = A.H / A.G, h0 = g * hpg + part * W.heads, h1 = min(h0 + W.heads, (g + 1) * hpg);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lg = lane >> 4, lr = lane & 15;
+  const int N = A.N, P = A.P, t0 = blk * Q, n = sequence_length(A.lengths, b, A.T);
+  const int here = min(max(n - t0, 0), Q), rows = min(A.T - t0, Q);
+  const long long row0 = (long long)b * A.T + t0;
+  const int pblocks = (P + kPB - 1) / kPB;
+
+  // where the sums of dC and dB go
+  const long long ldc = W.parts > 1 ? (long long)A.G * N : A.ld_c, ldb = W.parts > 1 ? (long long)A.G * N : A.ld_b;
+  const long long all = (long long)A.B * A.T * A.G * N;
+  float* dC = (W.parts > 1 ? W.part + 2 * part * all : A.dCm) + row0 * ldc + g * N;
+  float* dB = (W.parts > 1 ? W.part + (2 * part + 1) * all : A.dBm) + row0 * ldb + g * N;
+
+  if (here == 0) {  // padding: zeros
+    for (int i = tid; i < rows * (N / 4); i += kThreads) {
+      const int r = i / (N / 4), k = i % (N / 4) * 4;
+      *(float4*)(dC + r * ldc + k) = make_float4(0.f, 0.f, 0.f, 0.f);
+      *(float4*)(dB + r * ldb + k) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int j = 0; j < Q; ++j) {
-      const int t = blk * Q + (dir ? Q - 1 - j : j);
-      if (t >= n) continue;
-      const long long row = (long long)b * A.T + t;
-      const float dtv = softplus(A.dt[row * A.ld_dt + h] + bias);
-      const float a = expf(fmaxf(rate * dtv, -kMaxDecay));
+    for (int h = h0; h < h1; ++h) {
+      for (int i = tid; i < rows * (P / 4); i += kThreads)
+        *(float4*)(A.dx + (row0 + i / (P / 4)) * A.ld_x + h * P + i % (P / 4) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (tid < rows) A.ddt[(row0 + tid) * A.ld_dt + h] = 0.f;
+      if (tid < 3) W.sums[(((long long)b * W.blocks + blk) * A.H + h) * 3 + tid] = 0.0;
+    }
+    return;
+  }
+
+  auto put = [&](uint16_t* tile, int plane, int at, const uint4& v, bool whole) {
+    if (whole) {
+      *(uint4*)(tile + at) = v;
+    } else {
+      uint32_t a[3], d[3];
+      split_pair(__uint_as_float(v.x), __uint_as_float(v.y), a);
+      split_pair(__uint_as_float(v.z), __uint_as_float(v.w), d);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int k = lane + 64 * i;
-        if (k < A.N) {
-          if (dir) {
-            const float go = A.go[(((long long)b * A.H + h) * A.T + t) * A.P + p];
-            s[i] = a * (s[i] + go * scan_val<BF16>(A.Cm, row * A.ld_c + g * A.N + k));
-          } else {
-            const float x = scan_val<BF16>(A.x, row * A.ld_x + h * A.P + p);
-            s[i] = fmaf(a, s[i], dtv * x * scan_val<BF16>(A.Bm, row * A.ld_b + g * A.N + k));
+      for (int k = 0; k < 3; ++k) *(uint2*)(tile + k * plane + at) = make_uint2(a[k], d[k]);
+    }
+  };
+  constexpr int E = BF16 ? 8 : 4, ES = BF16 ? 2 : 4;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+
+  // ---- B, C of the block and G = C B^T, tile t = wave + 8 e as [j][i]
+  {
+    constexpr int KR = NK * 32 / E, KN = (Q * KR + kThreads - 1) / kThreads;
+#pragma unroll
+    for (int i = 0; i < KN; ++i) {
+      const int q = tid + kThreads * i, j = q / KR, k = q % KR * E;
+      if (j >= Q) break;
+      const bool in = j < here && k < N;
+      put(Bs, nB, j * LB + k, in ? *(const uint4*)((const char*)A.Bm + ((row0 + j) * A.ld_b + g * N + k) * ES) : zero, BF16);
+      put(Cs, nB, j * LB + k, in ? *(const uint4*)((const char*)A.Cm + ((row0 + j) * A.ld_c + g * N + k) * ES) : zero, BF16);
+    }
+  }
+  __syncthreads();
+  constexpr int MW = (MT + QT / 2 + kWaves - 1) / kWaves;  // tiles per wave, the zero tiles behind the others
+  int it_[MW], jt_[MW];
+  f32x4_t G[MW];
+#pragma unroll
+  for (int e = 0; e < MW; ++e) {
+    const int t = wave + kWaves * e;
+    int it = 1, jt = t - QT;
+    while (jt >= it) jt -= it++;
+    it_[e] = t < QT ? t : t < MT ? it : 2 * (t - MT);
+    jt_[e] = t < QT ? t : t < MT ? jt : 2 * (t - MT) + 1;
+    G[e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (t < MT) {
+#pragma unroll
+      for (int k = 0; k < NK; ++k)
+        mma(G[e], along<NP>(Bs + 16 * jt_[e] * LB + 32 * k, LB, nB, lane), along<NP>(Cs + 16 * it_[e] * LB + 32 * k, LB, nB, lane));
+    }
+  }
+
+  // ---- tiles of the results: dx as [channel][token], channel tile pt, token tiles jx ..; dC and dB as
+  // [d_k][token], d_k tile nt, token tiles ti ..
+  constexpr int JW = QT / 2, TG = kWaves / NT > 1 ? kWaves / NT : 1, TW = QT / TG > 0 ? QT / TG : 1;
+  const int pt = wave & 3, jx = (wave >> 2) * JW;
+  const int nt = wave % NT, ti = wave / NT * TW;
+  const bool owns = ti < QT;
+  f32x4_t sC[TW], sB[TW];
+#pragma unroll
+  for (int r = 0; r < TW; ++r) sC[r] = sB[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  constexpr int XR = kPB / E, XN = (Q * XR + kThreads - 1) / kThreads, GR = kPB / 4, GN = (Q * GR + kThreads - 1) / kThreads;
+  constexpr int UR = NK * 32 / 4, UN = kPB * UR / kThreads;
+  uint4 rx[XN], rg[GN];
+  auto fetch = [&](int h, int p0) {  // x and go of a head's channel block
+#pragma unroll
+    for (int i = 0; i < XN; ++i) {
+      const int q = tid + kThreads * i, j = q / XR, k = q % XR * E;
+      rx[i] = j < here && p0 + k < P ? *(const uint4*)((const char*)A.x + ((row0 + j) * A.ld_x + h * P + p0 + k) * ES) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < GN; ++i) {
+      const int q = tid + kThreads * i, j = q / GR, k = q % GR * 4;
+      rg[i] = j < here && p0 + k < P ? *(const uint4*)(A.go + (((long long)b * A.H + h) * A.T + t0 + j) * P + p0 + k) : zero;
+    }
+  };
+  auto put_xg = [&] {
+#pragma unroll
+    for (int i = 0; i < XN; ++i) {
+      const int q = tid + kThreads * i, j = q / XR, k = q % XR * E;
+      if (Q * XR % kThreads == 0 || j < Q) put(Xs, nX, j * LX + k, rx[i], BF16);
+    }
+#pragma unroll
+    for (int i = 0; i < GN; ++i) {
+      const int q = tid + kThreads * i, j = q / GR, k = q % GR * 4;
+      if (Q * GR % kThreads == 0 || j < Q) put(Gs, nX, j * LX + k, rg[i], false);
+    }
+  };
+
+  fetch(h0, 0);
+  for (int h = h0; h < h1; ++h) {
+    const long long bh = (long long)b * A.H + h;
+    const float D = A.D ? A.D[h] : 0.f;
+    const float* S = W.S + (bh * W.blocks + blk) * P * N;
+    const float* U = W.U + (bh * W.blocks + blk) * P * N;
+    // ---- gates, by every wave in its lanes, one of them each into LDS
+    const long long gate = bh * R.stride + t0 + (lane & (Q - 1));
+    const double l = R.l[gate];
+    const float step = R.step[gate];
+    const double end = read_lane(l, Q - 1);
+    __syncthreads();  // the head before is done
+    if (lane < Q) {
+      if (wave == 0) l_[lane] = l;
+      if (wave == 1) step_[lane] = step;
+      if (wave == 2) since_[lane] = exp2_of(l);
+      if (wave == 3) {
+        const float w = exp2_of(end - l);
+        w_[lane] = w;
+        left_[lane] = w * step;
+      }
+    }
+    double from = 0.0;
+#pragma unroll
+    for (int it = 1; it < QT; ++it) {
+      const double at = read_lane(l, 16 * it - 1);
+      from = lane >= 16 * it ? at : from;
+    }
+    if (wave == 7 && lane < Q) up_[lane] = exp2_of(l - from);
+
+    // ---- P = go x^T over the channel blocks; the last one's tiles stay
+    f32x4_t Pm[MW];
+#pragma unroll
+    for (int e = 0; e < MW; ++e) Pm[e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int pb = 0; pb < pblocks; ++pb) {
+      if (pb > 0) {
+        fetch(h, pb * kPB);
+        __syncthreads();  // the block before is read
+      }
+      put_xg();
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < MW; ++e)
+        if (wave + kWaves * e < MT) {
+#pragma unroll
+          for (int k = 0; k < kPB / 32; ++k)
+            mma(Pm[e], along<NP>(Xs + 16 * jt_[e] * LX + 32 * k, LX, nX, lane), along<3>(Gs + 16 * it_[e] * LX + 32 * k, LX, nX, lane));
+        }
+    }
+
+    // ---- M and R (R's columns in the order of across()), sums over rows and columns of F
+#pragma unroll
+    for (int e = 0; e < MW; ++e) {
+      const int t = wave + kWaves * e;
+      if (t >= MT + QT / 2) break;
+      const int i = 16 * it_[e] + lr, j = 16 * jt_[e] + 4 * lg;
+      float m[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};
+      if (t < MT) {
+        const bool diag = t < QT;
+        const f32x4_t st = *(const f32x4_t*)(step_ + j);
+        double row = 0.0, col[4];
+        float dec[4];  // E
+        if (diag) {
+          const double li = l_[i];
+          const double2 a0 = *(const double2*)(l_ + j), a1 = *(const double2*)(l_ + j + 2);
+          const double lj[4] = {a0.x, a0.y, a1.x, a1.y};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) dec[u] = exp2_of(li - lj[u]);
+        } else {
+          // over the start of the row's tile: both factors are at most 1
+          const double at = l_[16 * it_[e] - 1];
+          const double2 a0 = *(const double2*)(l_ + j), a1 = *(const double2*)(l_ + j + 2);
+          const double lj[4] = {a0.x, a0.y, a1.x, a1.y};
+          const float up = up_[i];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) dec[u] = up * exp2_of(at - lj[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t keep = !diag || j + u <= i ? ~0u : 0u, self = diag && j + u == i ? ~0u : 0u;
+          const float ge = __uint_as_float(__float_as_uint(G[e][u] * dec[u]) & keep);
+          const float pe = __uint_as_float(__float_as_uint(Pm[e][u] * dec[u]) & keep);
+          const float f = __uint_as_float(__float_as_uint(Pm[e][u] * ge) & keep);
+          m[u] = ge * st[u] + __uint_as_float(__float_as_uint(D) & self);
+          r[u] = pe * st[u];
+          if (self) {
+            diag_[i] = f;
+            trace_[i] = Pm[e][u];
           }
+          const double off = (double)__uint_as_float(__float_as_uint(f) & ~self);
+          col[u] = off;
+          row += off * (double)st[u];
+        }
+        // over the columns: the four groups of 16 lanes; over the rows: the lanes of a group
+        row += __shfl_xor(row, 16, 64);
+        row += __shfl_xor(row, 32, 64);
+        if (lg == 0) row_[t][lr] = row;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          double v = col[u];
+          v = add_dpp<0x111, 0xF>(v);
+          v = add_dpp<0x112, 0xF>(v);
+          v = add_dpp<0x114, 0xF>(v);
+          v = add_dpp<0x118, 0xF>(v);
+          if (lr == 15) col_[t][4 * lg + u] = v;
+        }
+      }
+      uint32_t a[3], d[3];
+      split_pair(m[0], m[1], a);
+      split_pair(m[2], m[3], d);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) *(uint2*)(Ms + k * nM + i * LM + j) = make_uint2(a[k], d[k]);
+      split_pair(r[0], r[1], a);
+      split_pair(r[2], r[3], d);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) *(uint2*)(Rs + k * nM + i * LM + across_order(j)) = make_uint2(a[k], d[k]);
+    }
+    __syncthreads();
+
+    // ---- inside the block: dC, dB; dx of every channel block, the one in LDS first
+    if (owns) {
+#pragma unroll
+      for (int r = 0; r < TW; ++r) {
+        const int t = ti + r;
+#pragma unroll
+        for (int k = 0; k < Q / 32; ++k) {
+          if (k <= t / 2) mma(sC[r], across<NP>(Bs + 32 * k * LB + 16 * nt, LB, nB, lane), along<3>(Rs + 16 * t * LM + 32 * k, LM, nM, lane));
+          if (k >= t / 2)
+            mma(sB[r], across<NP>(Cs + 32 * k * LB + 16 * nt, LB, nB, lane),
+                across<3, 8>(Rs + 32 * k * LM + 32 * (t >> 1) + 4 * (t & 1), LM, nM, lane));
         }
       }
     }
-  }
-  if (dir && A.ds_in) {
+    f32x4_t T1[TW], T2[TW];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (lane + 64 * i < A.N) A.ds_in[u * A.N + lane + 64 * i] = s[i];
+    for (int r = 0; r < TW; ++r) T1[r] = T2[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    double us = 0.0;
+    for (int q = 0; q < pblocks; ++q) {
+      const int pb = pblocks - 1 - q, p0 = pb * kPB;
+      f32x4_t dx[JW], du[JW];
+#pragma unroll
+      for (int r = 0; r < JW; ++r) dx[r] = du[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (q > 0) {
+        // (several channel blocks) M's place holds U of the block before: form it again from the registers
+        fetch(h, p0);
+        __syncthreads();
+        put_xg();
+#pragma unroll
+        for (int e = 0; e < MW; ++e) {
+          const int t = wave + kWaves * e;
+          if (t >= MT + QT / 2) break;
+          const int i = 16 * it_[e] + lr, j = 16 * jt_[e] + 4 * lg;
+          float m[4] = {0.f, 0.f, 0.f, 0.f};
+          if (t < MT) {
+            const bool diag = t < QT;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const double at = diag ? l_[i] : l_[16 * it_[e] - 1];
+              const float dec = exp2_of(at - l_[j + u]) * (diag ? 1.f : up_[i]);
+              const uint32_t keep = !diag || j + u <= i ? ~0u : 0u, self = diag && j + u == i ? ~0u : 0u;
+              const float ge = __uint_as_float(__float_as_uint(G[e][u] * dec) & keep);
+              m[u] = ge * step_[j + u] + __uint_as_float(__float_as_uint(D) & self);
+            }
+          }
+          uint32_t a[3], d[3];
+          split_pair(m[0], m[1], a);
+          split_pair(m[2], m[3], d);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) *(uint2*)(Ms + k * nM + i * LM + j) = make_uint2(a[k], d[k]);
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int r = 0; r < JW; ++r)
+#pragma unroll
+        for (int k = 0; k < Q / 32; ++k)
+          if (k >= (jx + r) / 2)
+            mma(dx[r], across<3, 8>(Gs + 32 * k * LX + 32 * (pt >> 1) + 4 * (pt & 1), LX, nX, lane),
+                across<3>(Ms + 32 * k * LM + 16 * (jx + r), LM, nM, lane));
+      // U of the channel block, its rows in the order in which across() takes them
+      uint4 ru[UN];
+#pragma unroll
+      for (int i = 0; i < UN; ++i) {
+        const int v = tid + kThreads * i, p = v / UR, k = v % UR * 4;
+        ru[i] = p0 + p < P && k < N ? *(const uint4*)(U + (long long)(p0 + p) * N + k) : zero;
+      }
+      __syncthreads();  // M and R are read
+#pragma unroll
+      for (int i = 0; i < UN; ++i) {
+        const int v = tid + kThreads * i, p = v / UR, k = v % UR * 4;
+        const int at = (p & 32) | ((p & 4) << 2) | ((p & 24) >> 1) | (p & 3);
+        put(Us, nU, at * LU + k, ru[i], false);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        const Frag<3> uf = along<3>(Us + 16 * pt * LU + 32 * k, LU, nU, lane);
+#pragma unroll
+        for (int r = 0; r < JW; ++r) mma(du[r], uf, along<NP>(Bs + 16 * (jx + r) * LB + 32 * k, LB, nB, lane));
+      }
+      if (owns) {
+#pragma unroll
+        for (int k = 0; k < kPB / 32; ++k) {
+          // S^T: d_k of this lane, 8 channels; and the same of U
+          float sv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          const int p = p0 + 32 * k + 8 * lg, kk = 16 * nt + lr;
+          if (p < P && kk < N) load8<false>(S, (long long)kk * P + p, sv);
+          const Frag<3> sf = split8(sv), uf = across<3>(Us + 32 * k * LU + 16 * nt, LU, nU, lane);
+          if (wave < NT) {
+            float uv[8];
+            values_of(uf, uv);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) us += (double)(uv[v] * sv[v]);
+          }
+#pragma unroll
+          for (int r = 0; r < TW; ++r) {
+            mma(T1[r], sf, along<3>(Gs + 16 * (ti + r) * LX + 32 * k, LX, nX, lane));
+            mma(T2[r], uf, along<NP>(Xs + 16 * (ti + r) * LX + 32 * k, LX, nX, lane));
+          }
+        }
+      }
+      const int pp = p0 + 32 * (pt >> 1) + 8 * lg + 4 * (pt & 1);
+#pragma unroll
+      for (int r = 0; r < JW; ++r) {
+        const int j = 16 * (jx + r) + lr;
+        if (j < rows && pp < P)
+          *(f32x4_t*)(A.dx + (row0 + j) * A.ld_x + h * P + pp) = j < here ? dx[r] + du[r] * left_[j] : f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+    }
+    if (h + 1 < h1) fetch(h + 1, 0);
+
+    // ---- the states' shares of dC and dB, and of the decays' gradients
+    if (owns) {
+#pragma unroll
+      for (int r = 0; r < TW; ++r) {
+        const int i = 16 * (ti + r) + lr;
+        const f32x4_t c1 = T1[r] * since_[i];
+        sC[r] += c1;
+        sB[r] += T2[r] * left_[i];
+        float cd = 0.f, bd = 0.f;
+#pragma unroll
+        for (int k = NP - 1; k >= 0; --k) {
+          const uint2 cv = *(const uint2*)(Cs + k * nB + i * LB + 16 * nt + 4 * lg), bv = *(const uint2*)(Bs + k * nB + i * LB + 16 * nt + 4 * lg);
+          cd += c1[0] * bf16lo(cv.x) + c1[1] * bf16hi(cv.x) + c1[2] * bf16lo(cv.y) + c1[3] * bf16hi(cv.y);
+          bd += T2[r][0] * bf16lo(bv.x) + T2[r][1] * bf16hi(bv.x) + T2[r][2] * bf16lo(bv.y) + T2[r][3] * bf16hi(bv.y);
+        }
+        cd = add_xor_f32(add_xor_f32(cd, 16), 32);
+        bd = add_xor_f32(add_xor_f32(bd, 16), 32);
+        if (lg == 0) {
+          read_[nt][i] = cd;
+          put_[nt][i] = bd * w_[i];
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) us += __shfl_xor(us, m, 64);
+    if (lane == 0) us_[wave] = us;
+    __syncthreads();
+
+    // ---- time steps: one token per lane of wave 0
+    if (wave == 0) {
+      const int i = lane & (Q - 1);
+      double row = 0.0, col = 0.0, rd = 0.0, pu = 0.0, whole = 0.0;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        int it = 1, jt = t - QT;
+        while (jt >= it) jt -= it++;
+        if (t < QT) it = jt = t;
+        row += i / 16 == it ? row_[t][i & 15] : 0.0;
+        col += i / 16 == jt ? col_[t][i & 15] : 0.0;
+      }
+      for (int k = 0; k < NT; ++k) {
+        rd += (double)read_[k][i];
+        pu += (double)put_[k][i];
+      }
+      for (int k = 0; k < kWaves; ++k) whole += us_[k];
+      const bool in = lane < here;
+      const float rate = -expf(A.A_log[h]);
+      const double st = (double)step;
+      const double ahead = in ? row - st * col + rd : 0.0, behind = in ? st * pu : 0.0;
+      const double pa = block_prefix<64>(ahead), pp = block_prefix<64>(behind);
+      const double dl = read_lane(pa, 63) - pa + ahead + pp - behind + (double)exp2_of(end) * whole;
+      double ddt = 0.0, da = 0.0, tr = 0.0;
+      if (in) {
+        const float raw = A.dt[(row0 + lane) * A.ld_dt + h] + A.dt_bias[h];
+        ddt = ((double)diag_[i] + col + pu + dl * (double)rate) * (double)(1.f / (1.f + expf(-raw)));
+        da = dl * (double)rate * st;
+        tr = (double)trace_[i];
+      }
+      if (lane < rows) A.ddt[(row0 + lane) * A.ld_dt + h] = (float)ddt;
+      const double s0 = read_lane(block_prefix<64>(da), 63), s1 = read_lane(block_prefix<64>(ddt), 63),
+                   s2 = read_lane(block_prefix<64>(tr), 63);
+      if (lane < 3) W.sums[(((long long)b * W.blocks + blk) * A.H + h) * 3 + lane] = lane == 0 ? s0 : lane == 1 ? s1 : s2;
+    }
+  }
+
+  if (owns) {
+    const int k = 16 * nt + 4 * lg;
+#pragma unroll
+    for (int r = 0; r < TW; ++r) {
+      const int i = 16 * (ti + r) + lr;
+      if (i < rows && k < N) {
+        *(f32x4_t*)(dC + i * ldc + k) = i < here ? sC[r] : f32x4_t{0.f, 0.f, 0.f, 0.f};
+        *(f32x4_t*)(dB + i * ldb + k) = i < here ? sB[r] : f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+    }
   }
 }
 
-// One workgroup per (sequence, block, group), the group's heads one after the other.
-template <bool BF16>
-__global__ void __launch_bounds__(256) scan_backward_kernel(ScanArgs A, ScanBwdWs W) {
-  __shared__ float Gm[Q][Q + 1], Pm[Q][Q + 1];
-  __shared__ double l[Q];
-  __shared__ float dtv[Q], slope[Q], read[Q], put[Q], q[Q];
-  __shared__ double red[4];
-  const int blk = blockIdx.x % W.nb, g = blockIdx.x / W.nb % A.G, b = blockIdx.x / W.nb / A.G;
-  const int n = sequence_length(A.lengths, b, A.T);
-  const int t0 = blk * Q, tid = threadIdx.x, N = A.N, P = A.P;
-  const int here = min(max(n - t0, 0), Q), rows = min(A.T - t0, Q);
-  auto xv = [&](int j, int h, int p) { return scan_val<BF16>(A.x, ((long long)b * A.T + t0 + j) * A.ld_x + h * P + p); };
-  auto bv = [&](int j, int k) { return scan_val<BF16>(A.Bm, ((long long)b * A.T + t0 + j) * A.ld_b + g * N + k); };
-  auto cv = [&](int j, int k) { return scan_val<BF16>(A.Cm, ((long long)b * A.T + t0 + j) * A.ld_c + g * N + k); };
-  for (int h = g * (A.H / A.G); h < (g + 1) * (A.H / A.G); ++h) {
-    const long long bh = (long long)b * A.H + h;
-    const float rate = -expf(A.A_log[h]), D = A.D ? A.D[h] : 0.f;
-    const float* S = W.S + (bh * W.nb + blk) * P * N;
-    const float* U = W.U + (bh * W.nb + blk) * P * N;
-    const float* go = A.go + (bh * A.T + t0) * P;
-    __syncthreads();
-    if (tid < Q) {
-      dtv[tid] = slope[tid] = 0.f;
-      if (tid < here) {
-        const float raw = A.dt[((long long)b * A.T + t0 + tid) * A.ld_dt + h] + A.dt_bias[h];
-        dtv[tid] = softplus(raw);
-        slope[tid] = 1.f / (1.f + expf(-raw));
-      }
-    }
-    __syncthreads();
-    if (tid == 0) {
-      double sum = 0.0;
-      for (int j = 0; j < Q; ++j) {
-        sum += (double)fmaxf(rate * dtv[j], -kMaxDecay);
-        l[j] = sum;
-      }
-    }
-    for (int e = tid; e < here * here; e += 256) {
-      const int i = e / here, j = e % here;
-      if (j > i) continue;
-      float gm = 0.f, pm = 0.f;
-      for (int k = 0; k < N; ++k) gm = fmaf(cv(i, k), bv(j, k), gm);
-      for (int p = 0; p < P; ++p) pm = fmaf(go[i * P + p], xv(j, h, p), pm);
-      Gm[i][j] = gm;
-      Pm[i][j] = pm;
-    }
-    __syncthreads();
-    for (int e = tid; e < here * here; e += 256) {
-      const int i = e / here, j = e % here;
-      if (j > i) continue;
-      Pm[i][j] *= (float)exp(l[i] - l[j]);
-    }
-    __syncthreads();
-    // dx
-    for (int e = tid; e < rows * P; e += 256) {
-      const int j = e / P, p = e % P;
-      float s = 0.f;
-      if (j < here) {
-        float ub = 0.f;
-        for (int k = 0; k < N; ++k) ub = fmaf(U[p * N + k], bv(j, k), ub);
-        s = (float)exp(l[Q - 1] - l[j]) * ub;
-        for (int i = j; i < here; ++i) s = fmaf(Gm[i][j] * (float)exp(l[i] - l[j]), go[i * P + p], s);
-        s = fmaf(dtv[j], s, D * go[j * P + p]);
-      }
-      A.dx[((long long)b * A.T + t0 + j) * A.ld_x + h * P + p] = s;
-    }
-    // dB and dC, added to those of the heads before
-    for (int e = tid; e < rows * N; e += 256) {
-      const int j = e / N, k = e % N;
-      float db = 0.f, dc = 0.f;
-      if (j < here) {
-        float ux = 0.f, sg = 0.f;
-        for (int p = 0; p < P; ++p) {
-          ux = fmaf(U[p * N + k], xv(j, h, p), ux);
-          sg = fmaf(S[p * N + k], go[j * P + p], sg);
-        }
-        db = (float)exp(l[Q - 1] - l[j]) * ux;
-        dc = (float)exp(l[j]) * sg;
-        for (int i = j; i < here; ++i) db = fmaf(Pm[i][j], cv(i, k), db);
-        for (int i = 0; i <= j; ++i) dc = fmaf(Pm[j][i] * dtv[i], bv(i, k), dc);
-        db *= dtv[j];
-      }
-      float* pb = A.dBm + ((long long)b * A.T + t0 + j) * A.ld_b + g * N + k;
-      float* pc = A.dCm + ((long long)b * A.T + t0 + j) * A.ld_c + g * N + k;
-      const bool add = h > g * (A.H / A.G);
-      *pb = add ? *pb + db : db;
-      *pc = add ? *pc + dc : dc;
-    }
-    // gradients of the decay
-    float us = 0.f, sd = 0.f;
-    for (int e = tid; e < P * N; e += 256) us = fmaf(U[e], S[e], us);
-    for (int e = tid; e < here * P; e += 256) sd = fmaf(go[e], xv(e / P, h, e % P), sd);
-    us = wave_sum_f32(us);
-    sd = wave_sum_f32(sd);
-    if ((tid & 63) == 0) red[tid >> 6] = us;
-    __syncthreads();
-    const double all = red[0] + red[1] + red[2] + red[3];
-    __syncthreads();
-    if ((tid & 63) == 0) red[tid >> 6] = sd;
-    if (tid < Q) {
-      float r = 0.f, w = 0.f, dq = 0.f;
-      if (tid < here) {
-        for (int p = 0; p < P; ++p) {
-          float sc = 0.f, ub = 0.f;
-          for (int k = 0; k < N; ++k) {
-            sc = fmaf(S[p * N + k], cv(tid, k), sc);
-            ub = fmaf(U[p * N + k], bv(tid, k), ub);
-          }
-          r = fmaf(go[tid * P + p], sc, r);
-          w = fmaf(xv(tid, h, p), ub, w);
-        }
-        r *= (float)exp(l[tid]);
-        w *= (float)exp(l[Q - 1] - l[tid]);
-        dq = w;
-        for (int i = tid; i < here; ++i) dq = fmaf(Pm[i][tid], Gm[i][tid], dq);
-      }
-      read[tid] = r;
-      put[tid] = w * dtv[tid];
-      q[tid] = dq;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      double dl = exp(l[Q - 1]) * all, da = 0.0, dbias = 0.0;
-      for (int j = 0; j < here; ++j) dl += (double)put[j];
-      // from the last token back
-      for (int t = here - 1; t >= 0; --t) {
-        dl += (double)read[t] - (double)put[t];
-        for (int j = 0; j < t; ++j) dl += (double)(Pm[t][j] * Gm[t][j] * dtv[j]);
-        for (int i = t + 1; i < here; ++i) dl -= (double)(Pm[i][t] * Gm[i][t] * dtv[t]);
-        const double d = ((double)q[t] + dl * rate) * slope[t];
-        A.ddt[((long long)b * A.T + t0 + t) * A.ld_dt + h] = (float)d;
-        da += dl * rate * dtv[t];
-        dbias += d;
-      }
-      for (int t = here; t < rows; ++t) A.ddt[((long long)b * A.T + t0 + t) * A.ld_dt + h] = 0.f;
-      double* out = W.sums + (((long long)b * W.nb + blk) * A.H + h) * 3;
-      out[0] = da;
-      out[1] = dbias;
-      out[2] = red[0] + red[1] + red[2] + red[3];
-    }
-  }
+// dC and dB from the parts of a group's heads, in their order
+__global__ void __launch_bounds__(256) scan_parts_kernel(ScanArgs A, ScanBwd W) {
+  const int per = A.G * A.N / 4;
+  const long long tokens = (long long)A.B * A.T, i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= 2 * tokens * per) return;
+  const int what = (int)(i / (tokens * per));
+  const long long at = i % (tokens * per), row = at / per;
+  const int k = (int)(at % per) * 4;
+  const f32x4_t* v = (const f32x4_t*)W.part + what * tokens * per + at;
+  f32x4_t s = v[0];
+  for (int p = 1; p < W.parts; ++p) s += v[2 * p * tokens * per];
+  *(f32x4_t*)((what ? A.dBm + row * A.ld_b : A.dCm + row * A.ld_c) + k) = s;
 }
 
 // Sums over sequences and blocks, in their order
-__global__ void __launch_bounds__(64) scan_sum_kernel(ScanArgs A, ScanBwdWs W) {
+__global__ void __launch_bounds__(64) scan_sum_kernel(ScanArgs A, ScanBwd W) {
   const int h = blockIdx.x, lane = threadIdx.x;
   double s[3] = {};
-  for (long long i = lane; i < (long long)A.B * W.nb; i += 64)
+  for (long long i = lane; i < (long long)A.B * W.blocks; i += 64)
     for (int k = 0; k < 3; ++k) s[k] += W.sums[(i * A.H + h) * 3 + k];
   for (int m = 32; m >= 1; m >>= 1)
     for (int k = 0; k < 3; ++k) s[k] += __shfl_xor(s[k], m, 64);
@@ -243,40 +516,117 @@ __global__ void __launch_bounds__(64) scan_sum_kernel(ScanArgs A, ScanBwdWs W) {
   }
 }
 
-size_t layout(const sdm_scan_shape& S, char* base, ScanBwdWs* W) {
-  const size_t nb = blocks_of(S.T), st = round_up((size_t)S.B * S.H * nb * S.d_v * S.d_k * 4);
-  W->nb = (int)nb;
-  W->S = (float*)base;
-  W->U = (float*)(base + st);
-  W->sums = (double*)(base + 2 * st);
-  return 2 * st + round_up((size_t)S.B * nb * S.H * 3 * 8);
+struct BwdPlan {
+  ScanGates gates;
+  ScanBwd bwd;
+  int segments;
+  float* first;
+  double* decay;
+  size_t bytes;
+};
+
+// A group's heads are shared out over workgroups until about two per compute unit are there.
+BwdPlan plan_of(const sdm_scan_shape& S, char* base) {
+  BwdPlan L{};
+  const int Q = S.in_dtype == SDM_BF16 ? 64 : 32, hpg = S.H / S.G;
+  const size_t units = (size_t)S.B * S.H, state = (size_t)S.d_v * S.d_k * 4;
+  L.bwd.blocks = (S.T + Q - 1) / Q;
+  const long long groups = (long long)S.B * S.G * L.bwd.blocks;
+  long long parts = groups > 0 ? (512 + groups - 1) / groups : 1;
+  if (parts > hpg) parts = hpg;
+  L.bwd.heads = (int)((hpg + parts - 1) / parts);
+  L.bwd.parts = (hpg + L.bwd.heads - 1) / L.bwd.heads;
+  L.segments = scan_segments((long long)units * ((S.d_v + kPB - 1) / kPB), L.bwd.blocks, 768);
+  size_t at = gates_bytes(units, S.T, base, &L.gates);
+  L.bwd.S = (float*)(base + at);
+  at += align_up(units * L.bwd.blocks * state);
+  L.bwd.U = (float*)(base + at);
+  at += align_up(units * L.bwd.blocks * state);
+  L.bwd.sums = (double*)(base + at);
+  at += align_up((size_t)S.B * L.bwd.blocks * S.H * 24);
+  if (L.bwd.parts > 1) {
+    L.bwd.part = (float*)(base + at);
+    at += align_up((size_t)L.bwd.parts * 2 * S.B * S.T * S.G * S.d_k * 4);
+  }
+  if (L.segments > 1) {
+    L.first = (float*)(base + at);
+    at += align_up(units * L.segments * state);
+    L.decay = (double*)(base + at);
+    at += align_up(units * L.segments * 8);
+  }
+  L.bytes = at + 256;  // (never empty)
+  return L;
+}
+
+template <bool BF16, int NK>
+hipError_t launch_main(const ScanArgs& A, const BwdPlan& L, hipStream_t stream) {
+  constexpr int lds = BwdTiles<BF16, NK>::bytes;
+  const long long grid = (long long)A.B * A.G * L.bwd.blocks * L.bwd.parts;
+  hipLaunchKernelGGL((scan_backward_kernel<BF16, NK>), dim3((unsigned)grid), dim3(kThreads), lds, stream, A, L.gates, L.bwd);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t scan_backward_workspace_bytes(const sdm_scan_shape& S) {
-  ScanBwdWs W;
-  return layout(S, nullptr, &W);
-}
+size_t scan_backward_workspace_bytes(const sdm_scan_shape& S) { return plan_of(S, nullptr).bytes; }
 
 hipError_t launch_scan_backward(const sdm_scan_shape& S, const ScanArgs& A, hipStream_t stream) {
-  ScanBwdWs W;
-  layout(S, (char*)A.ws, &W);
-  const dim3 waves((unsigned)(((long long)A.B * A.H * A.P + 3) / 4));
-  for (int dir = 0; dir < 2; ++dir) {
-    if (A.bf16) hipLaunchKernelGGL(scan_states_kernel<true>, waves, dim3(256), 0, stream, A, W, dir);
-    else hipLaunchKernelGGL(scan_states_kernel<false>, waves, dim3(256), 0, stream, A, W, dir);
-    const hipError_t e = hipGetLastError();
+  const BwdPlan L = plan_of(S, (char*)A.ws);
+  hipError_t e = launch_scan_gates(A, A.bf16 ? 64 : 32, L.gates, stream);
+  if (e != hipSuccess) return e;
+  ScanWalk K{};
+  K.B = A.B;
+  K.T = A.T;
+  K.H = A.H;
+  K.G = A.G;
+  K.N = A.N;
+  K.P = A.P;
+  K.blocks = L.bwd.blocks;
+  K.segments = L.segments;
+  K.stride = L.gates.stride;
+  K.lengths = A.lengths;
+  K.l = L.gates.l;
+  K.first = L.first;
+  K.decay = L.decay;
+  K.X = A.x;
+  K.K = A.Bm;
+  K.xb = (long long)A.T * A.ld_x;
+  K.xh = A.P;
+  K.ld_x = A.ld_x;
+  K.ld_k = A.ld_b;
+  K.weight = L.gates.left;
+  K.start = A.s_in;
+  K.states = (float*)L.bwd.S;
+  e = launch_scan_walk(K, A.bf16, false, stream);
+  if (e != hipSuccess) return e;
+  K.X = A.go;
+  K.K = A.Cm;
+  K.xb = (long long)A.H * A.T * A.P;
+  K.xh = (long long)A.T * A.P;
+  K.ld_x = A.P;
+  K.ld_k = A.ld_c;
+  K.weight = L.gates.since;
+  K.start = A.ds_out;
+  K.end = A.ds_in;
+  K.states = (float*)L.bwd.U;
+  e = launch_scan_walk(K, A.bf16, true, stream);
+  if (e != hipSuccess) return e;
+  if (L.bwd.blocks > 0) {
+    e = A.bf16   ? (A.N <= 32   ? launch_main<true, 1>(A, L, stream)
+                    : A.N <= 64 ? launch_main<true, 2>(A, L, stream)
+                                : launch_main<true, 4>(A, L, stream))
+        : A.N <= 32 ? launch_main<false, 1>(A, L, stream)
+        : A.N <= 64 ? launch_main<false, 2>(A, L, stream)
+                    : launch_main<false, 4>(A, L, stream);
     if (e != hipSuccess) return e;
+    if (L.bwd.parts > 1) {
+      const long long quads = 2ll * A.B * A.T * (A.G * A.N / 4);
+      hipLaunchKernelGGL(scan_parts_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, A, L.bwd);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
   }
-  if (W.nb > 0) {
-    const dim3 grid((unsigned)((long long)A.B * W.nb * A.G));
-    if (A.bf16) hipLaunchKernelGGL(scan_backward_kernel<true>, grid, dim3(256), 0, stream, A, W);
-    else hipLaunchKernelGGL(scan_backward_kernel<false>, grid, dim3(256), 0, stream, A, W);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(scan_sum_kernel, dim3(A.H), dim3(64), 0, stream, A, W);
+  hipLaunchKernelGGL(scan_sum_kernel, dim3(A.H), dim3(64), 0, stream, A, L.bwd);
   return hipGetLastError();
 }
 

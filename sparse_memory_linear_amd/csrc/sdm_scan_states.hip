@@ -1,0 +1,256 @@
+// Passes over the tokens of the selective scan that both its directions share: the time steps and
+// decays, and the walk that carries a state (or its gradient) from block to block.
+
+#include "sdm_device.hpp"
+#include "sdm_internal.hpp"
+#include "sdm_scan.hpp"
+
+namespace sdm {
+
+namespace {
+
+// ------------------------------------------------------------------ time steps
+// A workgroup takes 64 tokens of a sequence, all heads: dt comes in along the heads, goes through LDS and
+// is summed along the tokens, one per lane.
+template <int Q>
+__global__ void __launch_bounds__(256) scan_gates_kernel(ScanArgs A, ScanGates g) {
+  __shared__ float tile[64][65];
+  const int blocks = g.stride / 64, b = blockIdx.x / blocks, t0 = (int)(blockIdx.x % blocks) * 64;
+  const int here = min(max(sequence_length(A.lengths, b, A.T) - t0, 0), 64);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int h0 = 0; h0 < A.H; h0 += 64) {
+    const int heads = min(A.H - h0, 64);
+    __syncthreads();
+    for (int i = threadIdx.x; i < here * heads; i += 256)
+      tile[i / heads][i % heads] = A.dt[((long long)b * A.T + t0 + i / heads) * A.ld_dt + h0 + i % heads];
+    __syncthreads();
+    for (int h = wave; h < heads; h += 4) {
+      const float step = lane < here ? softplus(tile[lane][h] + A.dt_bias[h0 + h]) : 0.f;
+      const float la = lane < here ? fmaxf(-expf(A.A_log[h0 + h]) * step, -kMaxDecay) : 0.f;
+      const double l = block_prefix<Q>((double)la * kLog2e);
+      const double end = Q == 64 || lane >= 32 ? read_lane(l, 63) : read_lane(l, 31);
+      const long long at = ((long long)b * A.H + h0 + h) * g.stride + t0 + lane;
+      g.l[at] = l;
+      g.step[at] = step;
+      g.since[at] = exp2_of(l);
+      g.left[at] = exp2_of(end - l) * step;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the walk
+// S' = exp(l_end) S + sum_t (w_t X_t) K_t^T over the blocks of a segment of a (sequence, head, 64 channels)
+// unit, the state [d_v, d_k] in the accumulators of its matrix products: wave w holds channels
+// 16 w .. 16 w + 15, all d_k. Forward X = x, K = B, w = left; backward, from the last block to the first,
+// X = go, K = C, w = since. A block's loads are in flight while the block before is multiplied.
+//
+// With BLOCKS the state that enters each block is stored (backward: the gradient of the state after it):
+// forward as [d_k][d_v], backward as [d_v][d_k], the way the products that read it take it.
+constexpr int kPB = 64;
+
+template <int XP, int KP, int NK, bool BACK, bool BLOCKS>
+__global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
+  constexpr int Q = KP == 1 ? 64 : 32, NT = 2 * NK;
+  constexpr int LX = kPB + 16, LK = NK * 32 + 16, nX = Q * LX, nK = Q * LK;
+  constexpr bool TURN = BLOCKS && !BACK;  // results as [channel][d_k] tiles, else [d_k][channel]
+  extern __shared__ __align__(16) uint16_t lds[];
+  __shared__ __align__(16) float w_[Q];
+  uint16_t *Ks = lds, *Xs = Ks + KP * nK;
+
+  const int fast = A.B * A.G * A.segs, hpg = A.H / A.G;
+  const int f = blockIdx.x % fast, s = blockIdx.x / fast;
+  const int seg = f / (A.B * A.G), b = f % (A.B * A.G) / A.G, g = f % A.G;
+  const int h = g * hpg + s % hpg, pb = s / hpg, p0 = pb * kPB;
+  const long long bh = (long long)b * A.H + h;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lg = lane >> 4, lr = lane & 15;
+  const int n = sequence_length(A.lengths, b, A.T), N = A.N, P = A.P;
+  const int s0 = (int)((long long)A.blocks * seg / A.segments), s1 = (int)((long long)A.blocks * (seg + 1) / A.segments);
+
+  // 16-byte pieces: piece i of this thread is in row j + i (256 / pieces-per-row)
+  constexpr int XE = XP == 1 ? 8 : 4, KE = KP == 1 ? 8 : 4, XB = XP == 1 ? 2 : 4, KB = KP == 1 ? 2 : 4;
+  constexpr int XR = kPB / XE, KR = NK * 32 / KE, NX = Q * XR / 256, NKV = (Q * KR + 255) / 256, XS = 256 / XR, KS = 256 / KR;
+  const int xj = tid / XR, xk = (tid % XR) * XE, kj = tid / KR, kk = (tid % KR) * KE;
+  const bool xin = p0 + xk < P, kin = kk < N;
+  const char* px0 = (const char*)A.X + ((long long)b * A.xb + (long long)h * A.xh + p0) * XB;
+  const char* pk0 = (const char*)A.K + ((long long)b * A.T * A.ld_k + g * N) * KB;
+  const float* pw0 = A.weight + bh * A.stride;
+  const double* pl0 = A.l + bh * A.stride;
+  uint4 rx[NX], rk[NKV];
+  float rw = 0.f;
+  double rend = 0.0;
+  auto fetch = [&](int step) {
+    const int c = BACK ? A.blocks - 1 - step : step, here = min(max(n - c * Q, 0), Q);
+    const char* px = px0 + (long long)c * Q * A.ld_x * XB;
+    const char* pk = pk0 + (long long)c * Q * A.ld_k * KB;
+    const int xrows = xin ? here : 0, krows = kin ? here : 0;
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+      rx[i] = xj + i * XS < xrows ? *(const uint4*)(px + ((long long)(xj + i * XS) * A.ld_x + xk) * XB)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < NKV; ++i)
+      rk[i] = kj + i * KS < krows ? *(const uint4*)(pk + ((long long)(kj + i * KS) * A.ld_k + kk) * KB)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+    rw = pw0[c * Q + (lane & (Q - 1))];
+    rend = pl0[c * Q + Q - 1];
+  };
+  auto put = [&](uint16_t* tile, int plane, int at, const uint4& v, bool whole) {
+    if (whole) {
+      *(uint4*)(tile + at) = v;
+    } else {
+      uint32_t a[3], d[3];
+      split_pair(__uint_as_float(v.x), __uint_as_float(v.y), a);
+      split_pair(__uint_as_float(v.z), __uint_as_float(v.w), d);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) *(uint2*)(tile + k * plane + at) = make_uint2(a[k], d[k]);
+    }
+  };
+
+  // where this lane's value e of tile m lies in [d_v][d_k] (-1: nowhere)
+  auto place = [&](int m, int e) {
+    const int p = p0 + 16 * wave + (TURN ? 4 * lg + e : lr), k = 16 * m + (TURN ? lr : 4 * lg + e);
+    return p < P && k < N ? p * N + k : -1;
+  };
+  f32x4_t S[NT];
+  const float* from = A.segments > 1 && BLOCKS ? A.first + ((long long)seg * A.B * A.H + bh) * P * N
+                      : BLOCKS && A.start      ? A.start + bh * P * N
+                                               : nullptr;
+#pragma unroll
+  for (int m = 0; m < NT; ++m)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int at = place(m, e);
+      S[m][e] = from && at >= 0 ? from[at] : 0.f;
+    }
+  double total = 0.0;
+
+  if (s0 < s1) fetch(s0);
+  for (int step = s0; step < s1; ++step) {
+    const int c = BACK ? A.blocks - 1 - step : step;
+    if (BLOCKS) {
+      float* to = A.states + (bh * A.blocks + c) * P * N;
+      if (TURN) {  // [d_k][d_v]
+        const int p = p0 + 16 * wave + 4 * lg;
+#pragma unroll
+        for (int m = 0; m < NT; ++m)
+          if (p < P && 16 * m + lr < N) *(f32x4_t*)(to + (16 * m + lr) * P + p) = S[m];
+      } else {
+        const int p = p0 + 16 * wave + lr;
+#pragma unroll
+        for (int m = 0; m < NT; ++m)
+          if (p < P && 16 * m + 4 * lg < N) *(f32x4_t*)(to + p * N + 16 * m + 4 * lg) = S[m];
+      }
+    }
+    __syncthreads();  // the tiles of the block before are read
+#pragma unroll
+    for (int i = 0; i < NX; ++i) put(Xs, nX, (xj + i * XS) * LX + xk, rx[i], XP == 1);
+#pragma unroll
+    for (int i = 0; i < NKV; ++i)
+      if (Q * KR % 256 == 0 || kj + i * KS < Q) put(Ks, nK, (kj + i * KS) * LK + kk, rk[i], KP == 1);
+    if (wave == 0 && lane < Q) w_[lane] = rw;
+    const double end = rend;
+    if (step + 1 < s1) fetch(step + 1);
+    __syncthreads();
+    const float keep = exp2_of(end);
+    total += end;
+#pragma unroll
+    for (int m = 0; m < NT; ++m) S[m] *= keep;
+#pragma unroll
+    for (int k = 0; k < Q / 32; ++k) {
+      float v[8];
+      values_of(across<XP>(Xs + 32 * k * LX + 16 * wave, LX, nX, lane), v);
+      const f32x4_t w0 = *(const f32x4_t*)(w_ + 32 * k + 4 * lg), w1 = *(const f32x4_t*)(w_ + 32 * k + 16 + 4 * lg);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        v[u] *= w0[u];
+        v[4 + u] *= w1[u];
+      }
+      const Frag<3> xw = split8(v);
+      constexpr int MH = NT < 4 ? NT : 4;
+#pragma unroll
+      for (int m = 0; m < NT; m += MH) {
+        Frag<KP> kf[MH];
+#pragma unroll
+        for (int r = 0; r < MH; ++r) kf[r] = across<KP>(Ks + 32 * k * LK + 16 * (m + r), LK, nK, lane);
+        if (TURN) mma_rows<MH>(S + m, xw, kf);
+        else mma_cols<MH>(S + m, kf, xw);
+      }
+    }
+  }
+  float* to = !BLOCKS                     ? A.first + ((long long)(seg + 1) * A.B * A.H + bh) * P * N
+              : seg + 1 == A.segments && A.end ? A.end + bh * P * N
+                                               : nullptr;
+  if (to) {
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = place(m, e);
+        if (at >= 0) to[at] = S[m][e];
+      }
+  }
+  if (!BLOCKS && tid == 0 && pb == 0) A.decay[(long long)(seg + 1) * A.B * A.H + bh] = total;
+}
+
+// States before the segments, from the segments' own ends: first[0] is the call's first state, first[s]
+// (which holds what segment s-1 adds) takes up first[s-1] decayed over segment s-1.
+__global__ void __launch_bounds__(256) scan_join_kernel(ScanWalk A) {
+  const long long per = (long long)A.P * A.N / 4, units = (long long)A.B * A.H;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= units * per) return;
+  f32x4_t* v = (f32x4_t*)A.first;
+  f32x4_t s = A.start ? ((const f32x4_t*)A.start)[i] : f32x4_t{0.f, 0.f, 0.f, 0.f};
+  v[i] = s;
+  for (int k = 1; k < A.segments; ++k) {
+    s = v[k * units * per + i] + s * exp2_of(A.decay[k * units + i / per]);
+    v[k * units * per + i] = s;
+  }
+}
+
+template <int XP, int KP, int NK, bool BACK, bool BLOCKS>
+hipError_t launch_walk_kernel(ScanWalk A, hipStream_t stream) {
+  constexpr int Q = KP == 1 ? 64 : 32;
+  constexpr int lds = (KP * Q * (NK * 32 + 16) + XP * Q * (kPB + 16)) * 2;
+  A.segs = BLOCKS ? A.segments : A.segments - 1;
+  const long long units = (long long)A.B * A.H * ((A.P + kPB - 1) / kPB) * A.segs;
+  hipLaunchKernelGGL((scan_walk_kernel<XP, KP, NK, BACK, BLOCKS>), dim3((unsigned)units), dim3(256), lds, stream, A);
+  return hipGetLastError();
+}
+
+template <int XP, int KP, bool BACK, bool BLOCKS>
+hipError_t launch_walk_k(const ScanWalk& A, hipStream_t stream) {
+  return A.N <= 32   ? launch_walk_kernel<XP, KP, 1, BACK, BLOCKS>(A, stream)
+         : A.N <= 64 ? launch_walk_kernel<XP, KP, 2, BACK, BLOCKS>(A, stream)
+                     : launch_walk_kernel<XP, KP, 4, BACK, BLOCKS>(A, stream);
+}
+
+template <bool BLOCKS>
+hipError_t launch_walk_dir(const ScanWalk& A, bool bf16, bool back, hipStream_t stream) {
+  if (back) return bf16 ? launch_walk_k<3, 1, true, BLOCKS>(A, stream) : launch_walk_k<3, 3, true, BLOCKS>(A, stream);
+  return bf16 ? launch_walk_k<1, 1, false, BLOCKS>(A, stream) : launch_walk_k<3, 3, false, BLOCKS>(A, stream);
+}
+
+}  // namespace
+
+hipError_t launch_scan_gates(const ScanArgs& A, int Q, const ScanGates& g, hipStream_t stream) {
+  const dim3 grid((unsigned)((long long)A.B * (g.stride / 64)));
+  if (grid.x == 0) return hipSuccess;
+  if (Q == 64) hipLaunchKernelGGL(scan_gates_kernel<64>, grid, dim3(256), 0, stream, A, g);
+  else hipLaunchKernelGGL(scan_gates_kernel<32>, grid, dim3(256), 0, stream, A, g);
+  return hipGetLastError();
+}
+
+hipError_t launch_scan_walk(const ScanWalk& A, bool bf16, bool back, hipStream_t stream) {
+  hipError_t e = hipSuccess;
+  if (A.segments > 1) {
+    e = launch_walk_dir<false>(A, bf16, back, stream);
+    if (e != hipSuccess) return e;
+    const long long quads = (long long)A.B * A.H * A.P * A.N / 4;
+    hipLaunchKernelGGL(scan_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, A);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return A.states ? launch_walk_dir<true>(A, bf16, back, stream) : e;
+}
+
+}  // namespace sdm

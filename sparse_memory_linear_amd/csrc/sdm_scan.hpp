@@ -231,7 +231,9 @@ struct ScanWalk {
   float* end;          // state behind it, or null
   float* first;        // [segments][B*H][P][N]: states before the segments
   double* decay;       // [segments][B*H]: log2 of the segments' decay
-  float* states;       // [B*H][blocks][P N] states entering the blocks, or null: only `first` is wanted
+  // [B*H][blocks] states entering the blocks, forward [N][P] (as then `first` too), backward [P][N]; null: only
+  // `first` is wanted
+  float* states;
 };
 // Segments of a walk (or of the forward kernel): a call of few units is split until `wanted` workgroups are
 // busy, each with at least four blocks, so that enough share the pass that finds the segments' first states.

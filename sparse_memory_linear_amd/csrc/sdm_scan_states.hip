@@ -44,15 +44,15 @@ __global__ void __launch_bounds__(256) scan_gates_kernel(ScanArgs A, ScanGates g
 // 16 w .. 16 w + 15, all d_k. Forward X = x, K = B, w = left; backward, from the last block to the first,
 // X = go, K = C, w = since. A block's loads are in flight while the block before is multiplied.
 //
-// With BLOCKS the state that enters each block is stored (backward: the gradient of the state after it):
-// forward as [d_k][d_v], backward as [d_v][d_k], the way the products that read it take it.
+// With BLOCKS the state that enters each block is stored (backward: the gradient of the state after it).
+// TURN: results as [channel][d_k] tiles, whose lanes hold 4 consecutive channels, and states as [d_k][d_v]; else
+// the other way round. Each is stored the way the products that read it take it.
 constexpr int kPB = 64;
 
-template <int XP, int KP, int NK, bool BACK, bool BLOCKS>
+template <int XP, int KP, int NK, bool BACK, bool BLOCKS, bool TURN>
 __global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
   constexpr int Q = KP == 1 ? 64 : 32, NT = 2 * NK;
   constexpr int LX = kPB + 16, LK = NK * 32 + 16, nX = Q * LX, nK = Q * LK;
-  constexpr bool TURN = BLOCKS && !BACK;  // results as [channel][d_k] tiles, else [d_k][channel]
   extern __shared__ __align__(16) uint16_t lds[];
   __shared__ __align__(16) float w_[Q];
   uint16_t *Ks = lds, *Xs = Ks + KP * nK;
@@ -75,24 +75,25 @@ __global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
   const char* pk0 = (const char*)A.K + ((long long)b * A.T * A.ld_k + g * N) * KB;
   const float* pw0 = A.weight + bh * A.stride;
   const double* pl0 = A.l + bh * A.stride;
-  uint4 rx[NX], rk[NKV];
-  float rw = 0.f;
-  double rend = 0.0;
-  auto fetch = [&](int step) {
+  // two blocks ahead, in two sets of registers: a block's products are shorter than a load's way
+  uint4 rx[2][NX], rk[2][NKV];
+  float rw[2] = {0.f, 0.f};
+  double rend[2] = {0.0, 0.0};
+  auto fetch = [&](int step, int set) {
     const int c = BACK ? A.blocks - 1 - step : step, here = min(max(n - c * Q, 0), Q);
     const char* px = px0 + (long long)c * Q * A.ld_x * XB;
     const char* pk = pk0 + (long long)c * Q * A.ld_k * KB;
     const int xrows = xin ? here : 0, krows = kin ? here : 0;
 #pragma unroll
     for (int i = 0; i < NX; ++i)
-      rx[i] = xj + i * XS < xrows ? *(const uint4*)(px + ((long long)(xj + i * XS) * A.ld_x + xk) * XB)
+      rx[set][i] = xj + i * XS < xrows ? *(const uint4*)(px + ((long long)(xj + i * XS) * A.ld_x + xk) * XB)
                                   : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int i = 0; i < NKV; ++i)
-      rk[i] = kj + i * KS < krows ? *(const uint4*)(pk + ((long long)(kj + i * KS) * A.ld_k + kk) * KB)
+      rk[set][i] = kj + i * KS < krows ? *(const uint4*)(pk + ((long long)(kj + i * KS) * A.ld_k + kk) * KB)
                                   : make_uint4(0u, 0u, 0u, 0u);
-    rw = pw0[c * Q + (lane & (Q - 1))];
-    rend = pl0[c * Q + Q - 1];
+    rw[set] = pw0[c * Q + (lane & (Q - 1))];
+    rend[set] = pl0[c * Q + Q - 1];
   };
   auto put = [&](uint16_t* tile, int plane, int at, const uint4& v, bool whole) {
     if (whole) {
@@ -106,50 +107,48 @@ __global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
     }
   };
 
-  // where this lane's value e of tile m lies in [d_v][d_k] (-1: nowhere)
-  auto place = [&](int m, int e) {
-    const int p = p0 + 16 * wave + (TURN ? 4 * lg + e : lr), k = 16 * m + (TURN ? lr : 4 * lg + e);
-    return p < P && k < N ? p * N + k : -1;
+  // where the four values of tile m lie in a state of the walk's own layout (-1: nowhere)
+  auto place = [&](int m) {
+    const int p = p0 + 16 * wave + (TURN ? 4 * lg : lr), k = 16 * m + (TURN ? lr : 4 * lg);
+    return p < P && k < N ? (TURN ? k * P + p : p * N + k) : -1;
   };
   f32x4_t S[NT];
-  const float* from = A.segments > 1 && BLOCKS ? A.first + ((long long)seg * A.B * A.H + bh) * P * N
-                      : BLOCKS && A.start      ? A.start + bh * P * N
-                                               : nullptr;
+  const float* from = A.segments > 1 && BLOCKS ? A.first + ((long long)seg * A.B * A.H + bh) * P * N : nullptr;
+  const float* start = A.segments == 1 && A.start ? A.start + bh * P * N : nullptr;
 #pragma unroll
-  for (int m = 0; m < NT; ++m)
+  for (int m = 0; m < NT; ++m) {
+    const int at = place(m);
+    S[m] = from && at >= 0 ? *(const f32x4_t*)(from + at) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (start && at >= 0) {
+      if (TURN) {  // [d_v][d_k]
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int at = place(m, e);
-      S[m][e] = from && at >= 0 ? from[at] : 0.f;
+        for (int e = 0; e < 4; ++e) S[m][e] = start[(at % P + e) * N + at / P];
+      } else {
+        S[m] = *(const f32x4_t*)(start + at);
+      }
     }
+  }
   double total = 0.0;
 
-  if (s0 < s1) fetch(s0);
-  for (int step = s0; step < s1; ++step) {
+  auto block = [&](int step, int set) {
     const int c = BACK ? A.blocks - 1 - step : step;
     if (BLOCKS) {
       float* to = A.states + (bh * A.blocks + c) * P * N;
-      if (TURN) {  // [d_k][d_v]
-        const int p = p0 + 16 * wave + 4 * lg;
 #pragma unroll
-        for (int m = 0; m < NT; ++m)
-          if (p < P && 16 * m + lr < N) *(f32x4_t*)(to + (16 * m + lr) * P + p) = S[m];
-      } else {
-        const int p = p0 + 16 * wave + lr;
-#pragma unroll
-        for (int m = 0; m < NT; ++m)
-          if (p < P && 16 * m + 4 * lg < N) *(f32x4_t*)(to + p * N + 16 * m + 4 * lg) = S[m];
+      for (int m = 0; m < NT; ++m) {
+        const int at = place(m);
+        if (at >= 0) *(f32x4_t*)(to + at) = S[m];
       }
     }
     __syncthreads();  // the tiles of the block before are read
 #pragma unroll
-    for (int i = 0; i < NX; ++i) put(Xs, nX, (xj + i * XS) * LX + xk, rx[i], XP == 1);
+    for (int i = 0; i < NX; ++i) put(Xs, nX, (xj + i * XS) * LX + xk, rx[set][i], XP == 1);
 #pragma unroll
     for (int i = 0; i < NKV; ++i)
-      if (Q * KR % 256 == 0 || kj + i * KS < Q) put(Ks, nK, (kj + i * KS) * LK + kk, rk[i], KP == 1);
-    if (wave == 0 && lane < Q) w_[lane] = rw;
-    const double end = rend;
-    if (step + 1 < s1) fetch(step + 1);
+      if (Q * KR % 256 == 0 || kj + i * KS < Q) put(Ks, nK, (kj + i * KS) * LK + kk, rk[set][i], KP == 1);
+    if (wave == 0 && lane < Q) w_[lane] = rw[set];
+    const double end = rend[set];
+    if (step + 2 < s1) fetch(step + 2, set);
     __syncthreads();
     const float keep = exp2_of(end);
     total += end;
@@ -176,58 +175,78 @@ __global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
         else mma_cols<MH>(S + m, kf, xw);
       }
     }
+  };
+  if (s0 < s1) fetch(s0, 0);
+  if (s0 + 1 < s1) fetch(s0 + 1, 1);
+  for (int step = s0; step < s1; step += 2) {
+    block(step, 0);
+    if (step + 1 < s1) block(step + 1, 1);
   }
   float* to = !BLOCKS                     ? A.first + ((long long)(seg + 1) * A.B * A.H + bh) * P * N
               : seg + 1 == A.segments && A.end ? A.end + bh * P * N
                                                : nullptr;
-  if (to) {
+  if (to) {  // (a turned walk has no end)
 #pragma unroll
-    for (int m = 0; m < NT; ++m)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int at = place(m, e);
-        if (at >= 0) to[at] = S[m][e];
-      }
+    for (int m = 0; m < NT; ++m) {
+      const int at = place(m);
+      if (at >= 0) *(f32x4_t*)(to + at) = S[m];
+    }
   }
   if (!BLOCKS && tid == 0 && pb == 0) A.decay[(long long)(seg + 1) * A.B * A.H + bh] = total;
 }
 
 // States before the segments, from the segments' own ends: first[0] is the call's first state, first[s]
-// (which holds what segment s-1 adds) takes up first[s-1] decayed over segment s-1.
-__global__ void __launch_bounds__(256) scan_join_kernel(ScanWalk A) {
+// (which holds what segment s-1 adds) takes up first[s-1] decayed over segment s-1. `turned`: of [d_k][d_v].
+__global__ void __launch_bounds__(256) scan_join_kernel(ScanWalk A, bool turned) {
   const long long per = (long long)A.P * A.N / 4, units = (long long)A.B * A.H;
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   if (i >= units * per) return;
   f32x4_t* v = (f32x4_t*)A.first;
-  f32x4_t s = A.start ? ((const f32x4_t*)A.start)[i] : f32x4_t{0.f, 0.f, 0.f, 0.f};
+  f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+  if (A.start && turned) {
+    const long long unit = i / per;
+    const int at = (int)(i % per) * 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = A.start[unit * per * 4 + (at % A.P + e) * A.N + at / A.P];
+  } else if (A.start) {
+    s = ((const f32x4_t*)A.start)[i];
+  }
   v[i] = s;
-  for (int k = 1; k < A.segments; ++k) {
-    s = v[k * units * per + i] + s * exp2_of(A.decay[k * units + i / per]);
-    v[k * units * per + i] = s;
+  for (int k0 = 1; k0 < A.segments; k0 += 8) {  // eight loads in flight
+    f32x4_t add[8];
+    float keep[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const long long k = min(k0 + u, A.segments - 1);
+      add[u] = v[k * units * per + i];
+      keep[u] = exp2_of(A.decay[k * units + i / per]);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (k0 + u < A.segments) v[(k0 + u) * units * per + i] = s = add[u] + s * keep[u];
   }
 }
 
-template <int XP, int KP, int NK, bool BACK, bool BLOCKS>
+template <int XP, int KP, int NK, bool BACK, bool BLOCKS, bool TURN>
 hipError_t launch_walk_kernel(ScanWalk A, hipStream_t stream) {
   constexpr int Q = KP == 1 ? 64 : 32;
   constexpr int lds = (KP * Q * (NK * 32 + 16) + XP * Q * (kPB + 16)) * 2;
   A.segs = BLOCKS ? A.segments : A.segments - 1;
   const long long units = (long long)A.B * A.H * ((A.P + kPB - 1) / kPB) * A.segs;
-  hipLaunchKernelGGL((scan_walk_kernel<XP, KP, NK, BACK, BLOCKS>), dim3((unsigned)units), dim3(256), lds, stream, A);
+  hipLaunchKernelGGL((scan_walk_kernel<XP, KP, NK, BACK, BLOCKS, TURN>), dim3((unsigned)units), dim3(256), lds, stream, A);
   return hipGetLastError();
 }
 
-template <int XP, int KP, bool BACK, bool BLOCKS>
-hipError_t launch_walk_k(const ScanWalk& A, hipStream_t stream) {
-  return A.N <= 32   ? launch_walk_kernel<XP, KP, 1, BACK, BLOCKS>(A, stream)
-         : A.N <= 64 ? launch_walk_kernel<XP, KP, 2, BACK, BLOCKS>(A, stream)
-                     : launch_walk_kernel<XP, KP, 4, BACK, BLOCKS>(A, stream);
-}
-
-template <bool BLOCKS>
-hipError_t launch_walk_dir(const ScanWalk& A, bool bf16, bool back, hipStream_t stream) {
-  if (back) return bf16 ? launch_walk_k<3, 1, true, BLOCKS>(A, stream) : launch_walk_k<3, 3, true, BLOCKS>(A, stream);
-  return bf16 ? launch_walk_k<1, 1, false, BLOCKS>(A, stream) : launch_walk_k<3, 3, false, BLOCKS>(A, stream);
+template <bool BACK, bool BLOCKS, bool TURN>
+hipError_t launch_walk(const ScanWalk& A, bool bf16, hipStream_t stream) {
+  constexpr int XP = BACK ? 3 : 1;  // pieces of X beside bf16 inputs: go is float32
+  if (bf16)
+    return A.N <= 32   ? launch_walk_kernel<XP, 1, 1, BACK, BLOCKS, TURN>(A, stream)
+           : A.N <= 64 ? launch_walk_kernel<XP, 1, 2, BACK, BLOCKS, TURN>(A, stream)
+                       : launch_walk_kernel<XP, 1, 4, BACK, BLOCKS, TURN>(A, stream);
+  return A.N <= 32   ? launch_walk_kernel<3, 3, 1, BACK, BLOCKS, TURN>(A, stream)
+         : A.N <= 64 ? launch_walk_kernel<3, 3, 2, BACK, BLOCKS, TURN>(A, stream)
+                     : launch_walk_kernel<3, 3, 4, BACK, BLOCKS, TURN>(A, stream);
 }
 
 }  // namespace
@@ -241,16 +260,20 @@ hipError_t launch_scan_gates(const ScanArgs& A, int Q, const ScanGates& g, hipSt
 }
 
 hipError_t launch_scan_walk(const ScanWalk& A, bool bf16, bool back, hipStream_t stream) {
+  const bool turned = A.states && !back;
   hipError_t e = hipSuccess;
   if (A.segments > 1) {
-    e = launch_walk_dir<false>(A, bf16, back, stream);
+    e = back     ? launch_walk<true, false, false>(A, bf16, stream)
+        : turned ? launch_walk<false, false, true>(A, bf16, stream)
+                 : launch_walk<false, false, false>(A, bf16, stream);
     if (e != hipSuccess) return e;
     const long long quads = (long long)A.B * A.H * A.P * A.N / 4;
-    hipLaunchKernelGGL(scan_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, A);
+    hipLaunchKernelGGL(scan_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, A, turned);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  return A.states ? launch_walk_dir<true>(A, bf16, back, stream) : e;
+  if (!A.states) return e;
+  return back ? launch_walk<true, true, false>(A, bf16, stream) : launch_walk<false, true, true>(A, bf16, stream);
 }
 
 }  // namespace sdm

@@ -6,9 +6,9 @@
 //   dX[m] = sum_j w[c, j] dz[m + K-1 - j],  dw[c, j] = sum_t dz[t] X[t - (K-1) + j],  dbias = sum_t dz
 // and the last K-1 inputs, which are the state after the call, add ds_out.
 //
-// About 2 K operations for each value read and written, so memory bounds it. A thread takes 8
-// channels (one or two 16-byte accesses a row) of a run of tokens and slides over them with the
-// last K rows in registers.
+// About 2 K operations for each value read and written, so memory bounds it. A thread takes a few channels
+// (16-byte accesses) of a run of tokens: four tokens' loads are in flight while the four before are formed
+// from the last K-1 + 4 rows, which stay in registers.
 
 #include "sdm_device.hpp"
 #include "sdm_internal.hpp"
@@ -18,20 +18,46 @@ namespace sdm {
 namespace {
 
 constexpr int kRun = 16;      // tokens per thread
-constexpr int kBwdOct = 32;   // backward: channel octets per workgroup
-constexpr int kBwdRuns = 8;   // backward: token runs per workgroup
+constexpr int kStep = 4;      // tokens at a time
+constexpr int kBwdLanes = 64; // backward: threads along the channels, 4 channels each
+constexpr int kBwdRuns = 4;   // backward: token runs per workgroup
 
-// X[m] of 8 channels for m in [-(K-1), n): the state's rows before token 0, x behind them
-template <bool BF16, int K>
-__device__ __forceinline__ void load_x(const ConvArgs& A, int b, int m, int c0, float (&v)[8]) {
-  if (m >= 0) {
-    load8<BF16>(A.x, ((long long)b * A.T + m) * A.ld_x + c0, v);
-  } else if (A.s_in && m >= -(K - 1)) {
-    load8<BF16>(A.s_in, ((long long)b * (K - 1) + m + K - 1) * A.C + c0, v);
-  } else {
+// W consecutive channels of a row as they lie in memory
+template <bool BF16, int W>
+struct Row {
+  uint32_t q[BF16 ? W / 2 : W];
+  __device__ __forceinline__ void load(const void* base, long long at) {
+    const char* p = (const char*)base + at * (BF16 ? 2 : 4);
+    if (BF16 && W == 4) {
+      const uint2 v = *(const uint2*)p;
+      q[0] = v.x;
+      q[1] = v.y;
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+      for (int i = 0; i < (BF16 ? W / 2 : W) / 4; ++i) {
+        const uint4 v = *(const uint4*)(p + 16 * i);
+        q[4 * i] = v.x;
+        q[4 * i + 1] = v.y;
+        q[4 * i + 2] = v.z;
+        q[4 * i + 3] = v.w;
+      }
+    }
   }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? W / 2 : W); ++i) q[i] = 0u;
+  }
+  __device__ __forceinline__ float at(int e) const {
+    return BF16 ? ((e & 1) ? bf16hi(q[e >> 1]) : bf16lo(q[e >> 1])) : __uint_as_float(q[e]);
+  }
+};
+
+// X[m] of the channels from c0 for m in [-(K-1), n): the state's rows before token 0, x behind them; 0 elsewhere
+template <bool BF16, int K, int W>
+__device__ __forceinline__ void load_x(const ConvArgs& A, int b, int m, int n, int c0, Row<BF16, W>& r) {
+  if (m >= n || (m < 0 && (!A.s_in || m < -(K - 1)))) r.clear();
+  else if (m >= 0) r.load(A.x, ((long long)b * A.T + m) * A.ld_x + c0);
+  else r.load(A.s_in, ((long long)b * (K - 1) + m + K - 1) * A.C + c0);
 }
 
 // ------------------------------------------------------------------ forward
@@ -44,7 +70,18 @@ __global__ void __launch_bounds__(256) conv_kernel(ConvArgs A, int octets, long 
   const int c0 = (int)(u % octets) * 8;
   const int run = (int)(u / octets % runs), b = (int)(u / octets / runs);
   const int n = sequence_length(A.lengths, b, A.T);
-  const int t0 = run * kRun;
+  const int t0 = run * kRun, t1 = min(t0 + kRun, A.T);
+  Row<BF16, 8> next[kStep];
+  float win[K - 1 + kStep][8];  // X[t-(K-1)] .. X[t+kStep-1]
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) {
+    Row<BF16, 8> r;
+    load_x<BF16, K>(A, b, t0 - (K - 1) + j, n, c0, r);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) win[j][e] = r.at(e);
+  }
+#pragma unroll
+  for (int i = 0; i < kStep; ++i) load_x<BF16, K>(A, b, t0 + i, n, c0, next[i]);
   float w[K][8], bias[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -52,145 +89,172 @@ __global__ void __launch_bounds__(256) conv_kernel(ConvArgs A, int octets, long 
 #pragma unroll
     for (int j = 0; j < K; ++j) w[j][e] = A.w[(long long)(c0 + e) * K + j];
   }
-  float win[K][8];  // X[t-(K-1)] .. X[t]
-#pragma unroll
-  for (int j = 0; j < K - 1; ++j) {
-    const int m = t0 - (K - 1) + j;
-    if (m < n) load_x<BF16, K>(A, b, m, c0, win[j + 1]);
-  }
   if (run == 0 && A.s_out) {
     // the last K-1 inputs, all read before the first is written
-    float held[K - 1][8];
+    Row<BF16, 8> held[K - 1];
 #pragma unroll
-    for (int i = 0; i < K - 1; ++i) load_x<BF16, K>(A, b, n - (K - 1) + i, c0, held[i]);
+    for (int i = 0; i < K - 1; ++i) load_x<BF16, K>(A, b, n - (K - 1) + i, n, c0, held[i]);
 #pragma unroll
-    for (int i = 0; i < K - 1; ++i) store8<BF16>(A.s_out, ((long long)b * (K - 1) + i) * A.C + c0, held[i]);
+    for (int i = 0; i < K - 1; ++i) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = held[i].at(e);
+      store8<BF16>(A.s_out, ((long long)b * (K - 1) + i) * A.C + c0, v);
+    }
   }
-  const int t1 = min(t0 + kRun, A.T);
-  for (int t = t0; t < t1; ++t) {
-    float y[8];
-    if (t < n) {
+  for (int t = t0; t < t1; t += kStep) {
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j)
+    for (int i = 0; i < kStep; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) win[j][e] = win[j + 1][e];
-      load_x<BF16, K>(A, b, t, c0, win[K - 1]);
+      for (int e = 0; e < 8; ++e) win[K - 1 + i][e] = next[i].at(e);
+    if (t + kStep < t1) {
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) load_x<BF16, K>(A, b, t + kStep + i, n, c0, next[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) {
+      if (t + i >= t1) break;
+      float y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float z = bias[e];
 #pragma unroll
-        for (int j = 0; j < K; ++j) z = fmaf(w[j][e], win[j][e], z);
-        y[e] = A.silu ? z / (1.f + expf(-z)) : z;
+        for (int j = 0; j < K; ++j) z = fmaf(w[j][e], win[i + j][e], z);
+        y[e] = t + i < n ? (A.silu ? z * sigmoid_f32(z) : z) : 0.f;
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = 0.f;
+      store8<BF16>(A.y, ((long long)b * A.T + t + i) * A.ld_y + c0, y);
     }
-    store8<BF16>(A.y, ((long long)b * A.T + t) * A.ld_y + c0, y);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) win[j][e] = win[kStep + j][e];
   }
 }
 
 // ------------------------------------------------------------------ backward
-// A workgroup takes 32 octets and 8 consecutive runs of one sequence; its sums of dw and dbias
-// over those tokens go to one row of `part`, [workgroup][K+1][C].
+// A workgroup takes 256 channels and 4 consecutive runs of one sequence; its sums of dw and dbias over
+// those tokens go to one row of `part`, [workgroup][K+1][C].
 template <bool BF16, int K>
-__global__ void __launch_bounds__(kBwdOct * kBwdRuns) conv_backward_kernel(ConvArgs A, int groups) {
-  __shared__ float red[kBwdRuns][kBwdOct * 8];
-  const int oct = threadIdx.x % kBwdOct, sub = threadIdx.x / kBwdOct;
-  const int c0 = ((int)blockIdx.y * kBwdOct + oct) * 8;
+__global__ void __launch_bounds__(kBwdLanes * kBwdRuns) conv_backward_kernel(ConvArgs A, int groups) {
+  __shared__ float red[kBwdRuns][kBwdLanes * 4];
+  const int lane = threadIdx.x % kBwdLanes, sub = threadIdx.x / kBwdLanes;
+  const int c0 = ((int)blockIdx.y * kBwdLanes + lane) * 4;
   const int b = (int)(blockIdx.x / groups), group = (int)(blockIdx.x % groups);
   const int t0 = (group * kBwdRuns + sub) * kRun;
   const int n = sequence_length(A.lengths, b, A.T);
   const bool live = c0 < A.C;
-  float dw[K][8] = {}, db[8] = {};
+  float dw[K][4] = {}, db[4] = {};
   if (live && (t0 < A.T || t0 == 0)) {
-    float w[K][8], bias[8];
+    const int t1 = min(t0 + kRun, A.T), te = t1 + K - 1;
+    Row<BF16, 4> nx[kStep];
+    Row<false, 4> ny[kStep];
+    auto fetch = [&](int t) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+      for (int i = 0; i < kStep; ++i) {
+        load_x<BF16, K>(A, b, t + i, n, c0, nx[i]);
+        if (t + i < n) ny[i].load(A.dy, ((long long)b * A.T + t + i) * A.ld_y + c0);
+        else ny[i].clear();
+      }
+    };
+    float win[K - 1 + kStep][4], dz[K - 1 + kStep][4];  // X and dz from t-(K-1)
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      Row<BF16, 4> r;
+      load_x<BF16, K>(A, b, t0 - (K - 1) + j, n, c0, r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        win[j][e] = r.at(e);
+        dz[j][e] = 0.f;
+      }
+    }
+    fetch(t0);
+    float w[K][4], bias[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
       bias[e] = A.bias ? A.bias[c0 + e] : 0.f;
 #pragma unroll
       for (int j = 0; j < K; ++j) w[j][e] = A.w[(long long)(c0 + e) * K + j];
     }
-    float win[K][8], dz[K][8] = {};  // X[t-(K-1)] .. X[t]; dz[t-(K-1)] .. dz[t]
+    for (int t = t0; t < te; t += kStep) {
+      float dy[kStep][4];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) {
-      const int m = t0 - (K - 1) + j;
-      if (m < n) load_x<BF16, K>(A, b, m, c0, win[j + 1]);
-    }
-    const int t1 = min(t0 + kRun, A.T);
-    for (int t = t0; t < t1 + K - 1; ++t) {
+      for (int i = 0; i < kStep; ++i)
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          win[j][e] = win[j + 1][e];
-          dz[j][e] = dz[j + 1][e];
+        for (int e = 0; e < 4; ++e) {
+          win[K - 1 + i][e] = nx[i].at(e);
+          dy[i][e] = ny[i].at(e);
         }
-      if (t < n) {
-        load_x<BF16, K>(A, b, t, c0, win[K - 1]);
-        float dy[8];
-        load8<false>(A.dy, ((long long)b * A.T + t) * A.ld_y + c0, dy);
+      if (t + kStep < te) fetch(t + kStep);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float g = dy[e];
+      for (int i = 0; i < kStep; ++i) {
+        const bool own = t + i < t1;  // (dz of the tokens behind the run only serves dX)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float g = dy[i][e];
           if (A.silu) {
             float z = bias[e];
 #pragma unroll
-            for (int j = 0; j < K; ++j) z = fmaf(w[j][e], win[j][e], z);
-            const float s = 1.f / (1.f + expf(-z));
+            for (int j = 0; j < K; ++j) z = fmaf(w[j][e], win[i + j][e], z);
+            const float s = sigmoid_f32(z);
             g *= s * (1.f + z * (1.f - s));
           }
-          dz[K - 1][e] = g;
-          if (t < t1) {
+          g = t + i < n ? g : 0.f;
+          dz[K - 1 + i][e] = g;
+          if (own) {
             db[e] += g;
 #pragma unroll
-            for (int j = 0; j < K; ++j) dw[j][e] = fmaf(g, win[j][e], dw[j][e]);
+            for (int j = 0; j < K; ++j) dw[j][e] = fmaf(g, win[i + j][e], dw[j][e]);
           }
         }
-      } else {
+        // dz[m .. m+K-1] are known: dX[m]
+        const int m = t + i - (K - 1);
+        if (m >= t1 || (m < t0 && (t0 > 0 || !A.ds_in))) continue;
+        float dx[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dz[K - 1][e] = 0.f;
+        for (int e = 0; e < 4; ++e) {
+          dx[e] = 0.f;
+#pragma unroll
+          for (int j = 0; j < K; ++j) dx[e] = fmaf(w[j][e], dz[K - 1 - j + i][e], dx[e]);
+        }
+        const int q = m - n + K - 1;  // row of the final state that token m is
+        if (A.ds_out && q >= 0 && q < K - 1) {
+          const float4 ds = *(const float4*)(A.ds_out + ((long long)b * (K - 1) + q) * A.C + c0);
+          dx[0] += ds.x;
+          dx[1] += ds.y;
+          dx[2] += ds.z;
+          dx[3] += ds.w;
+        }
+        float* to = m >= 0 ? A.dx + ((long long)b * A.T + m) * A.ld_x + c0 : A.ds_in + ((long long)b * (K - 1) + m + K - 1) * A.C + c0;
+        *(float4*)to = make_float4(dx[0], dx[1], dx[2], dx[3]);
       }
-      // dz[m .. m+K-1] are known: dX[m]
-      const int m = t - (K - 1);
-      if (m < t0 && (t0 > 0 || !A.ds_in)) continue;
-      float dx[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dx[e] = 0.f;
+      for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-        for (int j = 0; j < K; ++j) dx[e] = fmaf(w[j][e], dz[K - 1 - j][e], dx[e]);
-      }
-      const int i = m - n + K - 1;  // row of the final state that token m is
-      if (A.ds_out && i >= 0 && i < K - 1) {
-        float ds[8];
-        load8<false>(A.ds_out, ((long long)b * (K - 1) + i) * A.C + c0, ds);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dx[e] += ds[e];
-      }
-      if (m >= 0) store8<false>(A.dx, ((long long)b * A.T + m) * A.ld_x + c0, dx);
-      else store8<false>(A.ds_in, ((long long)b * (K - 1) + m + K - 1) * A.C + c0, dx);
+        for (int e = 0; e < 4; ++e) {
+          win[j][e] = win[kStep + j][e];
+          dz[j][e] = dz[kStep + j][e];
+        }
     }
   }
-  // sums over the workgroup's runs, in their order
+  // sums over the workgroup's runs, in their order; one channel per thread
 #pragma unroll
   for (int j = 0; j <= K; ++j) {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[sub][oct * 8 + e] = j < K ? dw[j < K ? j : 0][e] : db[e];
+    for (int e = 0; e < 4; ++e) red[sub][lane * 4 + e] = j < K ? dw[j < K ? j : 0][e] : db[e];
     __syncthreads();
-    const int c = threadIdx.x;  // one channel per thread: kBwdOct * 8 == kBwdOct * kBwdRuns
+    const int c = threadIdx.x;
     float s = 0.f;
 #pragma unroll
     for (int r = 0; r < kBwdRuns; ++r) s += red[r][c];
-    const int ch = (int)blockIdx.y * kBwdOct * 8 + c;
+    const int ch = (int)blockIdx.y * kBwdLanes * 4 + c;
     if (ch < A.C) A.part[((long long)blockIdx.x * (K + 1) + j) * A.C + ch] = s;
   }
 }
-static_assert(kBwdOct * 8 == kBwdOct * kBwdRuns, "the reduction gives each thread one channel");
+static_assert(kBwdRuns == 4, "the reduction gives each thread one channel");
 
-// dw[c][j] and dbias[c] from the workgroups' sums, added in their order in float64: 64 columns x 4
-// row lanes per workgroup
+// dw[c][j] and dbias[c] from the workgroups' sums, added in their order in float64: 64 columns x 4 row lanes
+// per workgroup, eight loads of each in flight
 __global__ void __launch_bounds__(256) conv_sum_kernel(const float* part, float* dw, float* dbias, int C, int K,
                                                        long long n) {
   __shared__ double red[4][64];
@@ -198,7 +262,14 @@ __global__ void __launch_bounds__(256) conv_sum_kernel(const float* part, float*
   const int col = (int)blockIdx.x * 64 + lane, cols = (K + 1) * C;
   double s = 0.0;
   if (col < cols)
-    for (long long i = r; i < n; i += 4) s += (double)part[i * cols + col];
+    for (long long i = r; i < n; i += 32) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = part[min(i + 4 * u, n - 1) * cols + col];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i + 4 * u < n) s += (double)v[u];
+    }
   red[r][lane] = s;
   __syncthreads();
   if (r == 0 && col < cols) {
@@ -230,11 +301,11 @@ template <bool BF16>
 hipError_t launch_conv_backward_k(const ConvArgs& A, hipStream_t stream) {
   const int groups = conv_bwd_groups(A.T);
   const long long blocks = (long long)A.B * groups;
-  const dim3 grid((unsigned)blocks, (unsigned)((A.C / 8 + kBwdOct - 1) / kBwdOct));
+  const dim3 grid((unsigned)blocks, (unsigned)((A.C + kBwdLanes * 4 - 1) / (kBwdLanes * 4)));
   switch (A.K) {
 #define SDM_CONV(KK)                                                                                              \
   case KK:                                                                                                        \
-    hipLaunchKernelGGL((conv_backward_kernel<BF16, KK>), grid, dim3(kBwdOct * kBwdRuns), 0, stream, A, groups); \
+    hipLaunchKernelGGL((conv_backward_kernel<BF16, KK>), grid, dim3(kBwdLanes * kBwdRuns), 0, stream, A, groups); \
     break;
     SDM_CONV(2) SDM_CONV(3) SDM_CONV(4) SDM_CONV(5) SDM_CONV(6) SDM_CONV(7) SDM_CONV(8)
 #undef SDM_CONV

@@ -84,6 +84,12 @@ __device__ __forceinline__ int mbcnt(uint64_t m) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
 }
 
+// 1 / (1 + exp(-x)) on the hardware's exp2 and reciprocal (about 1 step each; the argument's rounding adds
+// |x| half steps to a value that is then below exp(-|x|))
+__device__ __forceinline__ float sigmoid_f32(float x) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * x));
+}
+
 // ------------------------------------------------------------------ rows of 8 values
 // 8 consecutive values of a bf16 or float32 row (16-byte aligned) as float32, and back.
 template <bool BF16>

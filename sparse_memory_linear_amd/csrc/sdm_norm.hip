@@ -34,7 +34,7 @@ __device__ __forceinline__ float act_of(int act, float g, float& slope) {
     slope = 1.f;
     return g;
   }
-  const float s = 1.f / (1.f + expf(-g));
+  const float s = sigmoid_f32(g);
   if (act == SDM_ACT_SIGMOID) {
     slope = s * (1.f - s);
     return s;
@@ -126,128 +126,192 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs A, long long per_ga
 }
 
 // ------------------------------------------------------------------ backward
-// Workgroup k of `parts` walks rows [M k / parts, M (k+1) / parts) and keeps their column sums in
-// registers. part[k][4][D]: the gate sums of a group of rows that begins before workgroup k's rows
-// and ends in them (0) or goes on behind them (1), dw_post (2) and dw_pre (3); a group that lies in
-// one workgroup's rows goes straight to dgate.
+// Workgroup k of `parts` takes rows [M k / parts, M (k+1) / parts) and keeps their column sums in
+// registers. WPR waves hold a row between them, NC octets a lane; a workgroup's row slots take its rows in
+// turn, so that with one wave a row no wave waits for another. part[k][4][D]: the gate sums of a group of
+// rows that begins before workgroup k's rows and ends in them (0) or goes on behind them (1), dw_post (2)
+// and dw_pre (3); a group that lies in one workgroup's rows goes straight to dgate.
 __device__ __forceinline__ long long part_begin(long long M, int k, int parts) { return M * k / parts; }
 
-template <int NC>
-__global__ void __launch_bounds__(1024) norm_backward_kernel(NormArgs A, long long per_gate, int parts) {
-  __shared__ float red[4][16];
-  const int octets = A.D / 8;
+template <int NC, int WPR>
+__global__ void __launch_bounds__(WPR > 4 ? 64 * WPR : 256, WPR > 8 ? 4 : NC * WPR > 4 ? 2 : 3) norm_backward_kernel(NormArgs A, long long per_gate, int parts) {
+  constexpr int WAVES = WPR > 4 ? WPR : 4, SLOTS = WAVES / WPR, LANES = 64 * WPR;
+  __shared__ float red[2][3][WAVES][2];  // by the row's parity: a row may have one meeting only
+  int turn = 0;
+  __shared__ __align__(16) float sums[SLOTS > 1 ? SLOTS * LANES * NC * 8 : 1];
+  const int octets = A.D / 8, wave = threadIdx.x >> 6, slot = wave / WPR, lane = threadIdx.x % LANES;
   const int k = blockIdx.x;
   const long long m0 = part_begin(A.M, k, parts), m1 = part_begin(A.M, k + 1, parts);
-  float sg[NC][8] = {}, sp[NC][8] = {}, sn[NC][8] = {};
   const float inv = 1.f / (float)A.D;
-  for (long long m = m0; m < m1; ++m) {
-    float yn[NC][8], h[NC][8], a[NC][8], t[NC][8];
-    float ss = 0.f;
-    __syncthreads();  // red is free again
+  // sums of two values over a row, the same in all its lanes
+  auto row_sum = [&](float& v, float& w, int which) {
+    v = wave_sum_f32(v);
+    w = wave_sum_f32(w);
+    if (WPR > 1) {
+      if ((threadIdx.x & 63) == 0) {
+        red[turn][which][wave][0] = v;
+        red[turn][which][wave][1] = w;
+      }
+      __syncthreads();
+      v = w = 0.f;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int o = threadIdx.x + i * blockDim.x;
-      if (o < octets) {
-        load8_rt(A.y, A.y_bf16, m * A.D + o * 8, yn[i]);
-        load8_rt(A.r, A.r_bf16, m * A.D + o * 8, h[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(yn[i][e], yn[i][e], ss);
+      for (int i = 0; i < WPR; ++i) {
+        v += red[turn][which][slot * WPR + i][0];
+        w += red[turn][which][slot * WPR + i][1];
       }
     }
-    float p = 1.f;
-    if (A.w_post) p = inv_rms(block_sum(ss, red[0]) * inv + A.eps);
-    float sr = 0.f, st = 0.f;
+  };
+  // column sums over the slots, in their order, to `to`
+  auto flush = [&](const float (&s)[NC][8], float* to) {
+    if (SLOTS > 1) {
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int o = threadIdx.x + i * blockDim.x;
-      if (o < octets) {
-        float w[8], g[8], dx[8], wn[8];
-        if (A.w_post) load8<false>(A.w_post, o * 8, w);
-        if (A.gate) load8_rt(A.gate, A.g_bf16, m / per_gate * A.D + o * 8, g);
-        if (A.w_pre) {
-          load8<false>(A.dx, m * A.D + o * 8, dx);
-          load8<false>(A.w_pre, o * 8, wn);
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sums[((slot * NC + i) * LANES + lane) * 8 + e] = s[i][e];
+      __syncthreads();
+      for (int q = threadIdx.x; q < octets * 2; q += 64 * WAVES) {  // 4 columns each
+        const int o = q >> 1, at = (o / LANES * LANES + o % LANES) * 8 + (q & 1) * 4;
+        float4 v = *(const float4*)(sums + at);
+        for (int r = 1; r < SLOTS; ++r) {
+          const float4 w = *(const float4*)(sums + r * NC * LANES * 8 + at);
+          v.x += w.x;
+          v.y += w.y;
+          v.z += w.z;
+          v.w += w.w;
         }
+        *(float4*)(to + o * 8 + (q & 1) * 4) = v;
+      }
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          yn[i][e] *= p;
-          float slope = 1.f;
-          a[i][e] = A.scale * (A.gate ? act_of(A.act, g[e], slope) : 1.f);
-          h[i][e] = fmaf(a[i][e], A.w_post ? yn[i][e] * w[e] : yn[i][e], h[i][e]);  // r'
-          t[i][e] = A.w_pre ? dx[e] * wn[e] : 0.f;
-          sr = fmaf(h[i][e], h[i][e], sr);
-          st = fmaf(t[i][e], h[i][e], st);
+      for (int i = 0; i < NC; ++i)
+        if (lane + i * LANES < octets) store8<false>(to, (lane + i * LANES) * 8, s[i]);
+    }
+  };
+
+  float sg[NC][8] = {}, sp[NC][8] = {}, sn[NC][8] = {};
+  const bool summed = A.gate && per_gate > 1;  // a gate of each token has no sums
+  for (long long g0 = m0; g0 < m1;) {
+    const long long grp = g0 / per_gate, end = summed ? (grp + 1) * per_gate : m1, g1 = end < m1 ? end : m1;
+    for (long long mm = g0; mm < g1; mm += SLOTS) {
+      const bool live = mm + slot < g1;
+      const long long m = live ? mm + slot : g1 - 1;
+      if (!live && WPR == 1) break;  // (with more waves a row all of them meet at the sums)
+      const long long gate_row = m / per_gate * A.D;
+      turn ^= 1;
+      float yn[NC][8], h[NC][8], t[NC][8], dr[NC][8];
+      float ss = 0.f, none = 0.f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int o = lane + i * LANES;
+        if (o < octets) {
+          load8_rt(A.y, A.y_bf16, m * A.D + o * 8, yn[i]);
+          load8_rt(A.r, A.r_bf16, m * A.D + o * 8, h[i]);
+          if (A.w_pre) load8<false>(A.dx, m * A.D + o * 8, t[i]);
+          if (A.dr_out) load8<false>(A.dr_out, m * A.D + o * 8, dr[i]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss = fmaf(yn[i][e], yn[i][e], ss);
+        }
+      }
+      float p = 1.f;
+      if (A.w_post) {
+        row_sum(ss, none, 0);
+        p = inv_rms(ss * inv + A.eps);
+      }
+      float sr = 0.f, st = 0.f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int o = lane + i * LANES;
+        if (o < octets) {
+          float w[8], g[8], wn[8];
+          if (A.w_post) load8<false>(A.w_post, o * 8, w);
+          if (A.gate) load8_rt(A.gate, A.g_bf16, gate_row + o * 8, g);
+          if (A.w_pre) load8<false>(A.w_pre, o * 8, wn);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            yn[i][e] *= p;
+            float slope = 1.f;
+            const float a = A.scale * (A.gate ? act_of(A.act, g[e], slope) : 1.f);
+            h[i][e] = fmaf(a, A.w_post ? yn[i][e] * w[e] : yn[i][e], h[i][e]);  // r'
+            if (A.w_pre) st = fmaf(t[i][e] * wn[e], h[i][e], st);
+            sr = fmaf(h[i][e], h[i][e], sr);
+          }
+        }
+      }
+      float q = 0.f, mean = 0.f;
+      if (A.w_pre) {
+        row_sum(sr, st, 1);
+        q = inv_rms(sr * inv + A.eps);
+        mean = st * q * inv;  // mean(t h)
+      }
+      float sy = 0.f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int o = lane + i * LANES;
+        if (o < octets) {
+          float w[8], g[8], wn[8], dg[8];
+          if (A.w_post) load8<false>(A.w_post, o * 8, w);
+          if (A.gate) load8_rt(A.gate, A.g_bf16, gate_row + o * 8, g);
+          if (A.w_pre) load8<false>(A.w_pre, o * 8, wn);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float d = A.dr_out ? dr[i][e] : 0.f;
+            if (A.w_pre) {
+              const float hn = h[i][e] * q;
+              d += q * (t[i][e] * wn[e] - hn * mean);
+              if (live) sn[i][e] = fmaf(t[i][e], hn, sn[i][e]);
+            }
+            dr[i][e] = d;
+            const float u = A.w_post ? yn[i][e] * w[e] : yn[i][e];
+            float slope = 0.f, a = A.scale;
+            if (A.gate) a *= act_of(A.act, g[e], slope);
+            dg[e] = A.scale * slope * u * d;
+            if (summed && live) sg[i][e] += dg[e];
+            const float du = a * d;
+            if (A.w_post && live) sp[i][e] = fmaf(du, yn[i][e], sp[i][e]);
+            t[i][e] = A.w_post ? du * w[e] : du;  // s
+            sy = fmaf(t[i][e], yn[i][e], sy);
+          }
+          if (live) {
+            store8<false>(A.dr, m * A.D + o * 8, dr[i]);
+            if (A.gate && !summed) store8<false>(A.dgate, m * A.D + o * 8, dg);
+          }
+        }
+      }
+      if (A.w_post) row_sum(sy, none, 2);
+      mean = sy * inv;
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int o = lane + i * LANES;
+          if (o < octets) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[i][e] = A.w_post ? p * (t[i][e] - yn[i][e] * mean) : t[i][e];
+            store8<false>(A.dy, m * A.D + o * 8, t[i]);
+          }
         }
       }
     }
-    float q = 0.f, mean = 0.f;
-    if (A.w_pre) {
-      q = inv_rms(block_sum(sr, red[1]) * inv + A.eps);
-      mean = block_sum(st, red[2]) * q * inv;  // mean(t h)
+    if (summed) {
+      flush(sg, grp * per_gate >= m0 && end <= m1 ? A.dgate + grp * A.D : A.part + ((long long)k * 4 + (end > m1 ? 1 : 0)) * A.D);
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sg[i][e] = 0.f;
     }
-    // the last row of its group, or of this workgroup: the gate's sums go out
-    const long long grp = m / per_gate, end = (grp + 1) * per_gate;
-    const bool flush = A.gate && (m + 1 == end || m + 1 == m1);
-    float* gate_to = grp * per_gate >= m0 && end <= m1 ? A.dgate + grp * A.D
-                                                       : A.part + ((long long)k * 4 + (end > m1 ? 1 : 0)) * A.D;
-    float sy = 0.f;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int o = threadIdx.x + i * blockDim.x;
-      if (o < octets) {
-        float w[8], g[8], dx[8], dr[8];
-        if (A.dr_out) load8<false>(A.dr_out, m * A.D + o * 8, dr);
-        if (A.w_post) load8<false>(A.w_post, o * 8, w);
-        if (A.gate) load8_rt(A.gate, A.g_bf16, m / per_gate * A.D + o * 8, g);
-        if (A.w_pre) load8<false>(A.dx, m * A.D + o * 8, dx);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          h[i][e] *= q;
-          const float d = (A.dr_out ? dr[e] : 0.f) + q * (t[i][e] - h[i][e] * mean);
-          dr[e] = d;
-          if (A.w_pre) sn[i][e] = fmaf(dx[e], h[i][e], sn[i][e]);
-          const float u = A.w_post ? yn[i][e] * w[e] : yn[i][e];
-          float slope = 0.f;
-          if (A.gate) act_of(A.act, g[e], slope);
-          if (A.gate) sg[i][e] = fmaf(A.scale * slope * u, d, sg[i][e]);
-          const float du = a[i][e] * d;
-          if (A.w_post) sp[i][e] = fmaf(du, yn[i][e], sp[i][e]);
-          t[i][e] = A.w_post ? du * w[e] : du;  // s
-          sy = fmaf(t[i][e], yn[i][e], sy);
-        }
-        store8<false>(A.dr, m * A.D + o * 8, dr);
-        if (flush) {
-          store8<false>(gate_to, o * 8, sg[i]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sg[i][e] = 0.f;
-        }
-      }
-    }
-    mean = A.w_post ? block_sum(sy, red[3]) * inv : 0.f;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int o = threadIdx.x + i * blockDim.x;
-      if (o < octets) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t[i][e] = A.w_post ? p * (t[i][e] - yn[i][e] * mean) : t[i][e];
-        store8<false>(A.dy, m * A.D + o * 8, t[i]);
-      }
-    }
+    g0 = g1;
   }
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int o = threadIdx.x + i * blockDim.x;
-    if (o < octets) {
-      if (A.w_post) store8<false>(A.part, ((long long)k * 4 + 2) * A.D + o * 8, sp[i]);
-      if (A.w_pre) store8<false>(A.part, ((long long)k * 4 + 3) * A.D + o * 8, sn[i]);
-    }
-  }
+  if (A.w_post) flush(sp, A.part + ((long long)k * 4 + 2) * A.D);
+  if (A.w_pre) flush(sn, A.part + ((long long)k * 4 + 3) * A.D);
 }
 
 // Column sums of the workgroups, in their order, in float64: dw_post (y = 0), dw_pre (y = 1) and, for
-// y = 2 + k, the gate group that begins in workgroup k's rows and goes on behind them, if there is one.
-__global__ void __launch_bounds__(256) norm_sum_kernel(NormArgs A, long long per_gate, int parts) {
-  __shared__ double red[4][64];
+// y >= 2, a gate group that workgroups share: group y - 2 (BY_GROUP: fewer groups than workgroups), or the one
+// that begins in the rows of workgroup y - 2 and goes on behind them, if there is one.
+// 64 columns x 16 row lanes, eight loads of each in flight: 512 rows are four round trips.
+template <bool BY_GROUP>
+__global__ void __launch_bounds__(1024) norm_sum_kernel(NormArgs A, long long per_gate, int parts) {
+  __shared__ double red[16][64];
   const int lane = threadIdx.x & 63, r = threadIdx.x >> 6;
   const int col = (int)blockIdx.x * 64 + lane;
   const int y = (int)blockIdx.y;
@@ -255,25 +319,47 @@ __global__ void __launch_bounds__(256) norm_sum_kernel(NormArgs A, long long per
   long long end = 0;
   float* out = y == 0 ? A.dw_post : A.dw_pre;
   if (y >= 2) {
-    k0 = y - 2;
-    const long long m0 = part_begin(A.M, k0, parts), m1 = part_begin(A.M, k0 + 1, parts);
-    if (m0 == m1) return;
-    const long long grp = (m1 - 1) / per_gate;
-    end = (grp + 1) * per_gate;
-    if (end <= m1 || grp * per_gate < m0) return;  // ends here, or began before
+    long long grp = y - 2;
+    if (BY_GROUP) {
+      // the workgroup that holds its first row
+      k0 = (int)(grp * per_gate * parts / A.M);
+      while (k0 + 1 < parts && part_begin(A.M, k0 + 1, parts) <= grp * per_gate) ++k0;
+      end = (grp + 1) * per_gate;
+      if (end <= part_begin(A.M, k0 + 1, parts)) return;  // no other holds any
+    } else {
+      k0 = y - 2;
+      const long long m0 = part_begin(A.M, k0, parts), m1 = part_begin(A.M, k0 + 1, parts);
+      if (m0 == m1) return;
+      grp = (m1 - 1) / per_gate;
+      end = (grp + 1) * per_gate;
+      if (end <= m1 || grp * per_gate < m0) return;  // ends here, or began before
+    }
     out = A.dgate + grp * A.D;
+    // the workgroup that holds its last row
+    k1 = (int)min((long long)parts, (end - 1) * parts / A.M + 2);
     while (k1 > k0 + 1 && part_begin(A.M, k1 - 1, parts) >= end) --k1;
   }
   if (!out) return;
   double s = 0.0;
   if (col < A.D)
-    for (int k = k0 + r; k < k1; k += 4) {
-      const int slot = y < 2 ? 2 + y : end > part_begin(A.M, k + 1, parts) ? 1 : 0;
-      s += (double)A.part[((long long)k * 4 + slot) * A.D + col];
+    for (int kk = k0 + r; kk < k1; kk += 128) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int k = min(kk + 16 * u, k1 - 1);
+        const int slot = y < 2 ? 2 + y : end > part_begin(A.M, k + 1, parts) ? 1 : 0;
+        v[u] = A.part[((long long)k * 4 + slot) * A.D + col];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (kk + 16 * u < k1) s += (double)v[u];
     }
   red[r][lane] = s;
   __syncthreads();
-  if (r == 0 && col < A.D) out[col] = (float)(((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane]);
+  if (r == 0 && col < A.D) {
+    for (int i = 1; i < 16; ++i) s += red[i][lane];
+    out[col] = (float)s;
+  }
 }
 
 // Workgroup width and octets per thread for rows of D values
@@ -285,13 +371,17 @@ void row_plan(int D, int* threads, int* nc) {
   *threads = t;
 }
 
-// Workgroups of the backward pass: every one has a row
-int backward_parts(long long M) { return (int)(M < 1 ? 1 : M < 512 ? M : 512); }
+// Workgroups of the backward pass: as many as are resident at once (three per compute unit while four waves
+// hold a row or several, two of 8, one of 16), so that few partial sums are written; every one has a row
+int backward_parts(long long M, int D) {
+  const int most = D <= 2048 ? 768 : D <= 8192 ? 512 : 256;
+  return (int)(M < 1 ? 1 : M < most ? M : most);
+}
 
 }  // namespace
 
 size_t norm_backward_workspace_bytes(const sdm_norm_shape& S) {
-  return align_up((size_t)backward_parts(S.M) * 4 * S.D * 4);
+  return align_up((size_t)backward_parts(S.M, S.D) * 4 * S.D * 4);
 }
 
 hipError_t launch_norm(const NormArgs& A, hipStream_t stream) {
@@ -305,22 +395,31 @@ hipError_t launch_norm(const NormArgs& A, hipStream_t stream) {
 }
 
 hipError_t launch_norm_backward(const NormArgs& A, hipStream_t stream) {
-  int threads, nc;
-  row_plan(A.D, &threads, &nc);
-  const int parts = backward_parts(A.M);
+  const int parts = backward_parts(A.M, A.D), octets = A.D / 8;
   const long long per = A.gate_rows > 0 && A.M > 0 ? A.M / A.gate_rows : 1;
-  const dim3 grid((unsigned)parts), block((unsigned)threads);
-  if (nc == 1) hipLaunchKernelGGL(norm_backward_kernel<1>, grid, block, 0, stream, A, per, parts);
-  else hipLaunchKernelGGL(norm_backward_kernel<2>, grid, block, 0, stream, A, per, parts);
+#define SDM_NORM(NC, WPR)                                                                                            \
+  hipLaunchKernelGGL((norm_backward_kernel<NC, WPR>), dim3((unsigned)parts), dim3(WPR > 4 ? 64 * WPR : 256), 0, stream, \
+                     A, per, parts)
+  if (octets <= 64) SDM_NORM(1, 1);
+  else if (octets <= 128) SDM_NORM(1, 2);
+  else if (octets <= 256) SDM_NORM(1, 4);
+  else if (octets <= 512) SDM_NORM(1, 8);
+  else if (octets <= 1024) SDM_NORM(2, 8);
+  else SDM_NORM(2, 16);
+#undef SDM_NORM
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (A.M == 0 && A.gate) {
     e = launch_zero(A.dgate, (size_t)A.gate_rows * A.D / 2, stream);
     if (e != hipSuccess) return e;
   }
+  const int cols = (A.D + 63) / 64;
   const bool gate_sums = A.gate && A.M > 0 && per > 1;
-  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((A.D + 63) / 64), (unsigned)(2 + (gate_sums ? parts : 0))),
-                     dim3(256), 0, stream, A, per, parts);
+  if (gate_sums && A.gate_rows >= parts)
+    hipLaunchKernelGGL(norm_sum_kernel<false>, dim3(cols, 2 + parts), dim3(1024), 0, stream, A, per, parts);
+  else
+    hipLaunchKernelGGL(norm_sum_kernel<true>, dim3(cols, 2 + (gate_sums ? (int)A.gate_rows : 0)), dim3(1024), 0, stream, A, per,
+                       parts);
   return hipGetLastError();
 }
 

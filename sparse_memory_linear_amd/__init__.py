@@ -361,51 +361,69 @@ def recurrent_chunked(shape: Shape, widx, wgt, ridx, rgt, v, alpha, beta, M, o, 
 
 
 # ----------------------------------------------------------------------------- convolution, scan, norm
+_torch = None  # torch, and the types of the tensors by the sdm_dtype: looked up once, on the first call
+_TYPES = ()
+
+
+def _load_torch():
+    global _torch, _TYPES
+    import torch
+    _TYPES = (torch.float32, torch.bfloat16, torch.int32)
+    _torch = torch
+
+
+_I32 = 2  # index of int32 among the types
+
+
 class _Args:
-    """Pointers of one call's tensors: each checked for dtype, shape and strides, and for lying on the
-    one GPU of the call, before the library sees an address."""
+    """Pointers of one call's tensors: each checked for type, shape and strides, and for lying on the one
+    GPU of the call, before the library sees an address."""
+    __slots__ = ("where", "device")
 
     def __init__(self, where: str):
-        self.where, self.device = where, None
+        if _torch is None:
+            _load_torch()
+        self.where, self.device = where, -1
 
-    def _take(self, name, t, dtype, optional):
-        import torch
+    def _take(self, name, t, dtype):
         if t is None:
-            if not optional:
-                raise ValueError(f"{self.where}: {name} is missing")
-            return None
-        want = (torch.float32, torch.bfloat16)[dtype] if isinstance(dtype, int) else dtype
-        if t.dtype != want:
+            raise ValueError(f"{self.where}: {name} is missing")
+        want = _TYPES[dtype] if 0 <= dtype < len(_TYPES) else f"of sdm_dtype {dtype}"
+        if t.dtype is not want:
             raise ValueError(f"{self.where}: {name} is {t.dtype}, not {want}")
-        if not t.is_cuda:
-            raise ValueError(f"{self.where}: {name} is not on a GPU")
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{self.where}: {name} is on {t.device}, another tensor on {self.device}")
+        d = t.get_device()
+        if d != self.device or d < 0:
+            if d < 0:
+                raise ValueError(f"{self.where}: {name} is not on a GPU")
+            if self.device >= 0:
+                raise ValueError(f"{self.where}: {name} is on GPU {d}, another tensor on GPU {self.device}")
+            self.device = d
         return t.data_ptr()
 
-    def flat(self, name, t, dtype, *shape, optional=False):
+    def flat(self, name, t, dtype, *shape):
         """A contiguous tensor of `shape`."""
-        p = self._take(name, t, dtype, optional)
-        if t is not None and (t.shape != shape or not t.is_contiguous()):
+        p = self._take(name, t, dtype)
+        if t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{self.where}: {name} has shape {tuple(t.shape)} and strides {t.stride()}, not a "
                              f"contiguous {shape}")
         return p
 
+    def maybe(self, name, t, dtype, *shape):
+        """The same, or None."""
+        return None if t is None else self.flat(name, t, dtype, *shape)
+
     def rows(self, name, t, dtype, B, T, width, ld):
         """[B, T, width], or [B, T, ...] with the last dimensions flattened to `width`: rows `ld` apart."""
-        p = self._take(name, t, dtype, False)
-        ok = t.dim() >= 3 and t.shape[0] == B and t.shape[1] == T
+        p = self._take(name, t, dtype)
+        shape, stride = t.shape, t.stride()
+        ok = len(shape) >= 3 and shape[0] == B and shape[1] == T
         inner = 1
-        if ok:
-            for d in range(t.dim() - 1, 1, -1):
-                ok = ok and (t.shape[d] == 1 or t.stride(d) == inner)
-                inner *= t.shape[d]
-            ok = ok and inner == width and (T <= 1 or t.stride(1) == ld) and (B == 1 or T == 0 or
-                                                                              t.stride(0) == T * ld)
+        for d in range(len(shape) - 1, 1, -1):
+            ok = ok and (shape[d] == 1 or stride[d] == inner)
+            inner *= shape[d]
+        ok = ok and inner == width and (T <= 1 or stride[1] == ld) and (B == 1 or T == 0 or stride[0] == T * ld)
         if not ok:
-            raise ValueError(f"{self.where}: {name} has shape {tuple(t.shape)} and strides {t.stride()}, not rows of "
+            raise ValueError(f"{self.where}: {name} has shape {tuple(shape)} and strides {stride}, not rows of "
                              f"{width} values with token stride {ld} for B={B}, T={T}")
         return p
 
@@ -413,26 +431,27 @@ class _Args:
         """(pointer, bytes) of the workspace; its size is checked by the library."""
         if ws is None:
             return None, 0
-        p = self._take("ws", ws, ws.dtype, False)
-        if not ws.is_contiguous():
-            raise ValueError(f"{self.where}: ws is not contiguous")
-        return p, ws.numel() * ws.element_size()
+        d = ws.get_device()
+        if d < 0 or (self.device >= 0 and d != self.device) or not ws.is_contiguous():
+            raise ValueError(f"{self.where}: ws is not a contiguous tensor on the GPU of the call")
+        return ws.data_ptr(), ws.numel() * ws.element_size()
 
     def call(self, shape, stream, *args):
         """Runs the entry point on `stream`, or on the current stream of the tensors' GPU."""
-        import torch
-        f = getattr(lib(), self.where)
-        dev = self.device
-        if dev is None or dev.index == torch.cuda.current_device():
-            _check(f(ctypes.byref(shape), *args, _stream(stream)), self.where)
-            return
-        with torch.cuda.device(dev):
-            _check(f(ctypes.byref(shape), *args, _stream(stream)), self.where)
-
-
-def _i32():
-    import torch
-    return torch.int32
+        f, dev, cuda = getattr(lib(), self.where), self.device, _torch.cuda
+        if dev < 0:
+            dev = cuda.current_device()
+        if stream is None:
+            stream = _torch._C._cuda_getCurrentRawStream(dev)
+        elif not isinstance(stream, int):
+            stream = stream.cuda_stream
+        if dev == cuda.current_device():
+            code = f(ctypes.byref(shape), *args, stream)
+        else:
+            with cuda.device(dev):
+                code = f(ctypes.byref(shape), *args, stream)
+        if code != 0:
+            raise SdmError(code, self.where)
 
 
 def make_conv_shape(B, T, C, K, in_dtype=SDM_BF16, act=SDM_ACT_SILU, ld_x=None, ld_y=None) -> ConvShape:
@@ -447,16 +466,16 @@ def check_conv_shape(shape: ConvShape) -> int:
 def short_conv(shape: ConvShape, x, w, y, bias=None, lengths=None, s_in=None, s_out=None, stream=None):
     s, a = shape, _Args("sdm_short_conv")
     a.call(s, stream, a.rows("x", x, s.in_dtype, s.B, s.T, s.C, s.ld_x), a.flat("w", w, SDM_F32, s.C, s.K),
-           a.flat("bias", bias, SDM_F32, s.C, optional=True), a.flat("lengths", lengths, _i32(), s.B, optional=True),
-           a.flat("s_in", s_in, s.in_dtype, s.B, s.K - 1, s.C, optional=True),
-           a.flat("s_out", s_out, s.in_dtype, s.B, s.K - 1, s.C, optional=True),
+           a.maybe("bias", bias, SDM_F32, s.C), a.maybe("lengths", lengths, _I32, s.B),
+           a.maybe("s_in", s_in, s.in_dtype, s.B, s.K - 1, s.C),
+           a.maybe("s_out", s_out, s.in_dtype, s.B, s.K - 1, s.C),
            a.rows("y", y, s.in_dtype, s.B, s.T, s.C, s.ld_y))
 
 
 def short_conv_step(shape: ConvShape, x, w, state, y, bias=None, stream=None):
     s, a = shape, _Args("sdm_short_conv_step")
     a.call(s, stream, a.rows("x", x, s.in_dtype, s.B, s.T, s.C, s.ld_x), a.flat("w", w, SDM_F32, s.C, s.K),
-           a.flat("bias", bias, SDM_F32, s.C, optional=True),
+           a.maybe("bias", bias, SDM_F32, s.C),
            a.flat("state", state, s.in_dtype, s.B, s.K - 1, s.C), a.rows("y", y, s.in_dtype, s.B, s.T, s.C, s.ld_y))
 
 
@@ -468,13 +487,13 @@ def short_conv_backward(shape: ConvShape, x, w, dy, dx, dw, ws, bias=None, dbias
                         ds_out=None, ds_in=None, stream=None):
     s, a = shape, _Args("sdm_short_conv_backward")
     a.call(s, stream, a.rows("x", x, s.in_dtype, s.B, s.T, s.C, s.ld_x), a.flat("w", w, SDM_F32, s.C, s.K),
-           a.flat("bias", bias, SDM_F32, s.C, optional=True), a.flat("lengths", lengths, _i32(), s.B, optional=True),
-           a.flat("s_in", s_in, s.in_dtype, s.B, s.K - 1, s.C, optional=True),
+           a.maybe("bias", bias, SDM_F32, s.C), a.maybe("lengths", lengths, _I32, s.B),
+           a.maybe("s_in", s_in, s.in_dtype, s.B, s.K - 1, s.C),
            a.rows("dy", dy, SDM_F32, s.B, s.T, s.C, s.ld_y),
-           a.flat("ds_out", ds_out, SDM_F32, s.B, s.K - 1, s.C, optional=True),
+           a.maybe("ds_out", ds_out, SDM_F32, s.B, s.K - 1, s.C),
            a.rows("dx", dx, SDM_F32, s.B, s.T, s.C, s.ld_x), a.flat("dw", dw, SDM_F32, s.C, s.K),
-           a.flat("dbias", dbias, SDM_F32, s.C, optional=True),
-           a.flat("ds_in", ds_in, SDM_F32, s.B, s.K - 1, s.C, optional=True), *a.workspace(ws))
+           a.maybe("dbias", dbias, SDM_F32, s.C),
+           a.maybe("ds_in", ds_in, SDM_F32, s.B, s.K - 1, s.C), *a.workspace(ws))
 
 
 def make_scan_shape(B, T, H, G, d_k, d_v, in_dtype=SDM_BF16, ld_x=None, ld_b=None, ld_c=None, ld_dt=None) -> ScanShape:
@@ -492,7 +511,7 @@ def _scan_inputs(a: _Args, s: ScanShape, x, Bm, Cm, dt, A_log, dt_bias, D):
             a.rows("Bm", Bm, s.in_dtype, s.B, s.T, s.G * s.d_k, s.ld_b),
             a.rows("Cm", Cm, s.in_dtype, s.B, s.T, s.G * s.d_k, s.ld_c), a.rows("dt", dt, SDM_F32, s.B, s.T, s.H, s.ld_dt),
             a.flat("A_log", A_log, SDM_F32, s.H), a.flat("dt_bias", dt_bias, SDM_F32, s.H),
-            a.flat("D", D, SDM_F32, s.H, optional=True))
+            a.maybe("D", D, SDM_F32, s.H))
 
 
 def selective_scan_workspace_bytes(shape: ScanShape) -> int:
@@ -504,8 +523,8 @@ def selective_scan(shape: ScanShape, x, Bm, Cm, dt, A_log, dt_bias, o, ws, D=Non
     s, a = shape, _Args("sdm_selective_scan")
     state = (s.B, s.H, s.d_v, s.d_k)
     a.call(s, stream, *_scan_inputs(a, s, x, Bm, Cm, dt, A_log, dt_bias, D),
-           a.flat("lengths", lengths, _i32(), s.B, optional=True),
-           a.flat("s_in", s_in, SDM_F32, *state, optional=True), a.flat("s_out", s_out, SDM_F32, *state, optional=True),
+           a.maybe("lengths", lengths, _I32, s.B),
+           a.maybe("s_in", s_in, SDM_F32, *state), a.maybe("s_out", s_out, SDM_F32, *state),
            a.flat("o", o, SDM_F32, s.B, s.H, s.T, s.d_v), *a.workspace(ws))
 
 
@@ -524,15 +543,15 @@ def selective_scan_backward(shape: ScanShape, x, Bm, Cm, dt, A_log, dt_bias, go,
     s, a = shape, _Args("sdm_selective_scan_backward")
     state = (s.B, s.H, s.d_v, s.d_k)
     a.call(s, stream, *_scan_inputs(a, s, x, Bm, Cm, dt, A_log, dt_bias, D),
-           a.flat("lengths", lengths, _i32(), s.B, optional=True),
-           a.flat("s_in", s_in, SDM_F32, *state, optional=True), a.flat("go", go, SDM_F32, s.B, s.H, s.T, s.d_v),
-           a.flat("ds_out", ds_out, SDM_F32, *state, optional=True),
+           a.maybe("lengths", lengths, _I32, s.B),
+           a.maybe("s_in", s_in, SDM_F32, *state), a.flat("go", go, SDM_F32, s.B, s.H, s.T, s.d_v),
+           a.maybe("ds_out", ds_out, SDM_F32, *state),
            a.rows("dx", dx, SDM_F32, s.B, s.T, s.H * s.d_v, s.ld_x),
            a.rows("dBm", dBm, SDM_F32, s.B, s.T, s.G * s.d_k, s.ld_b),
            a.rows("dCm", dCm, SDM_F32, s.B, s.T, s.G * s.d_k, s.ld_c),
            a.rows("ddt", ddt, SDM_F32, s.B, s.T, s.H, s.ld_dt), a.flat("dA_log", dA_log, SDM_F32, s.H),
-           a.flat("ddt_bias", ddt_bias, SDM_F32, s.H), a.flat("dD", dD, SDM_F32, s.H, optional=True),
-           a.flat("ds_in", ds_in, SDM_F32, *state, optional=True), *a.workspace(ws))
+           a.flat("ddt_bias", ddt_bias, SDM_F32, s.H), a.maybe("dD", dD, SDM_F32, s.H),
+           a.maybe("ds_in", ds_in, SDM_F32, *state), *a.workspace(ws))
 
 
 def make_norm_shape(M, D, y_dtype=SDM_F32, r_dtype=SDM_F32, x_dtype=SDM_BF16, gate_dtype=SDM_F32, gate_rows=0,
@@ -548,9 +567,9 @@ def check_norm_shape(shape: NormShape) -> int:
 def block_norm(shape: NormShape, y, r, r_out, gate=None, w_post=None, w_pre=None, x=None, stream=None):
     s, a = shape, _Args("sdm_block_norm")
     a.call(s, stream, a.flat("y", y, s.y_dtype, s.M, s.D), a.flat("r", r, s.r_dtype, s.M, s.D),
-           a.flat("gate", gate, s.gate_dtype, s.gate_rows, s.D, optional=True),
-           a.flat("w_post", w_post, SDM_F32, s.D, optional=True), a.flat("w_pre", w_pre, SDM_F32, s.D, optional=True),
-           a.flat("r_out", r_out, s.r_dtype, s.M, s.D), a.flat("x", x, s.x_dtype, s.M, s.D, optional=True))
+           a.maybe("gate", gate, s.gate_dtype, s.gate_rows, s.D),
+           a.maybe("w_post", w_post, SDM_F32, s.D), a.maybe("w_pre", w_pre, SDM_F32, s.D),
+           a.flat("r_out", r_out, s.r_dtype, s.M, s.D), a.maybe("x", x, s.x_dtype, s.M, s.D))
 
 
 def block_norm_backward_workspace_bytes(shape: NormShape) -> int:
@@ -561,10 +580,10 @@ def block_norm_backward(shape: NormShape, y, r, dy, dr, ws, gate=None, w_post=No
                         dgate=None, dw_post=None, dw_pre=None, stream=None):
     s, a = shape, _Args("sdm_block_norm_backward")
     a.call(s, stream, a.flat("y", y, s.y_dtype, s.M, s.D), a.flat("r", r, s.r_dtype, s.M, s.D),
-           a.flat("gate", gate, s.gate_dtype, s.gate_rows, s.D, optional=True),
-           a.flat("w_post", w_post, SDM_F32, s.D, optional=True), a.flat("w_pre", w_pre, SDM_F32, s.D, optional=True),
-           a.flat("dr_out", dr_out, SDM_F32, s.M, s.D, optional=True), a.flat("dx", dx, SDM_F32, s.M, s.D, optional=True),
+           a.maybe("gate", gate, s.gate_dtype, s.gate_rows, s.D),
+           a.maybe("w_post", w_post, SDM_F32, s.D), a.maybe("w_pre", w_pre, SDM_F32, s.D),
+           a.maybe("dr_out", dr_out, SDM_F32, s.M, s.D), a.maybe("dx", dx, SDM_F32, s.M, s.D),
            a.flat("dy", dy, SDM_F32, s.M, s.D), a.flat("dr", dr, SDM_F32, s.M, s.D),
-           a.flat("dgate", dgate, SDM_F32, s.gate_rows, s.D, optional=True),
-           a.flat("dw_post", dw_post, SDM_F32, s.D, optional=True), a.flat("dw_pre", dw_pre, SDM_F32, s.D, optional=True),
+           a.maybe("dgate", dgate, SDM_F32, s.gate_rows, s.D),
+           a.maybe("dw_post", dw_post, SDM_F32, s.D), a.maybe("dw_pre", dw_pre, SDM_F32, s.D),
            *a.workspace(ws))

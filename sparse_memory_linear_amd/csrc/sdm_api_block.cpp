@@ -70,8 +70,8 @@ sdm_status check_conv(const sdm_conv_shape* S) {
   if (S->K < 2 || S->K > 8 || S->C % 8 != 0 || S->ld_x % 8 != 0 || S->ld_y % 8 != 0) return SDM_ERR_UNSUPPORTED;
   if (S->C > (1 << 20) || S->ld_x > kMaxStride || S->ld_y > kMaxStride) return SDM_ERR_UNSUPPORTED;
   if ((int64_t)S->B * S->T > kMaxTokens) return SDM_ERR_UNSUPPORTED;
-  // grids: one thread per 16 tokens of 8 channels, one workgroup per 64 tokens
-  if ((int64_t)S->B * (S->T / 16 + 1) > ((int64_t)1 << 31) / (S->C / 8) ||
+  // grids: one thread per 16 tokens of 4 channels, one workgroup per 64 tokens
+  if ((int64_t)S->B * (S->T / 16 + 1) > ((int64_t)1 << 31) / (S->C / 4) ||
       (int64_t)S->B * (S->T / 64 + 1) > (1 << 23))
     return SDM_ERR_UNSUPPORTED;
   return SDM_OK;

@@ -76,15 +76,15 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   const float D = A.D ? A.D[h] : 0.f;
 
   // 16-byte pieces of a block's tiles: piece i of this thread lies in row j + i (256 / pieces-per-row) for
-  // its row j of piece 0, in the same columns; `in` is what the columns allow
+  // its row j of piece 0, in the same columns
   constexpr int E = BF16 ? 8 : 4, ES = BF16 ? 2 : 4;        // values per piece, bytes per value
   constexpr int XR = kPB / E, KR = NK * 32 / E;             // pieces per row
   constexpr int NX = Q * XR / 256, NKV = (Q * KR + 255) / 256;      // pieces per thread
   constexpr int XS = 256 / XR, KS = 256 / KR;               // rows between pieces
   const int xj = tid / XR, xk = (tid % XR) * E, kj = tid / KR, kk = (tid % KR) * E;
-  const bool xin = p0 + xk < P, kin = kk < N;
-  const uint32_t xoff = (uint32_t)(xj * A.ld_x + xk) * ES, boff = (uint32_t)(kj * A.ld_b + kk) * ES,
-                 coff = (uint32_t)(kj * A.ld_c + kk) * ES;
+  const uint32_t xoff = p0 + xk < P ? (uint32_t)(xj * A.ld_x + xk) * ES : kNowhere,
+                 boff = kk < N ? (uint32_t)(kj * A.ld_b + kk) * ES : kNowhere,
+                 coff = kk < N ? (uint32_t)(kj * A.ld_c + kk) * ES : kNowhere;
   const uint32_t xstep = (uint32_t)(XS * A.ld_x) * ES, bstep = (uint32_t)(KS * A.ld_b) * ES,
                  cstep = (uint32_t)(KS * A.ld_c) * ES;
   uint4 rx[NX], rb[NKV], rc[NKV];
@@ -102,33 +102,17 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   };
   // part `part` of `parts` of a block's pieces, `here` of its tokens inside the sequence
   auto fetch = [&](int here, int part, int parts) {
-    // kept as one 32-bit offset beside a scalar base, instead of a 64-bit address of each piece in registers
-    uint32_t xo = xoff, bo = boff, co = coff;
-    asm volatile("" : "+v"(xo), "+v"(bo), "+v"(co));
-    if (wide && here == Q && Q * KR % 256 == 0) {
+    const rsrc_t rows_x = block_rows(px, (uint32_t)(here * A.ld_x) * ES), rows_b = block_rows(pB, (uint32_t)(here * A.ld_b) * ES),
+                 rows_c = block_rows(pC, (uint32_t)(here * A.ld_c) * ES);
 #pragma unroll
-      for (int i = 0; i < NKV; ++i)
-        if (i % parts == part) {
-          rb[i] = *(const uint4*)(pB + (bo + i * bstep));
-          rc[i] = *(const uint4*)(pC + (co + i * cstep));
-        }
+    for (int i = 0; i < NKV; ++i)
+      if (i % parts == part) {
+        rb[i] = load16(rows_b, boff + i * bstep);
+        rc[i] = load16(rows_c, coff + i * cstep);
+      }
 #pragma unroll
-      for (int i = 0; i < NX; ++i)
-        if (i % parts == part) rx[i] = *(const uint4*)(px + (xo + i * xstep));
-    } else {
-      const int xrows = xin ? here : 0, krows = kin ? here : 0;
-#pragma unroll
-      for (int i = 0; i < NKV; ++i)
-        if (i % parts == part) {
-          const bool in = kj + i * KS < krows;
-          rb[i] = in ? *(const uint4*)(pB + (bo + i * bstep)) : make_uint4(0u, 0u, 0u, 0u);
-          rc[i] = in ? *(const uint4*)(pC + (co + i * cstep)) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-      for (int i = 0; i < NX; ++i)
-        if (i % parts == part)
-          rx[i] = xj + i * XS < xrows ? *(const uint4*)(px + (xo + i * xstep)) : make_uint4(0u, 0u, 0u, 0u);
-    }
+    for (int i = 0; i < NX; ++i)
+      if (i % parts == part) rx[i] = load16(rows_x, xoff + i * xstep);
   };
   // the block's gates, one token per lane
   double rl = 0.0;
@@ -385,19 +369,17 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
     }
     // the state at the block's end
     constexpr int MH = NT < 4 ? NT : 4;  // tiles of d_k at a time
-    Frag<NP> bf[2][MH];
+    Frag<NP> bf[MH];
     auto load_b = [&](int s) {  // step s: 32 tokens, MH tiles
       const int k = s / (NT / MH), m0 = s % (NT / MH) * MH;
 #pragma unroll
       for (int m = 0; m < MH; ++m)
-        bf[s & 1][m] = across<NP, 8>(Bs + 32 * k * LB + 32 * ((m0 + m) >> 1) + 4 * (m & 1), LB, nB, lane);
+        bf[m] = across<NP, 8>(Bs + 32 * k * LB + 32 * ((m0 + m) >> 1) + 4 * (m & 1), LB, nB, lane);
     };
-    load_b(0);
 #pragma unroll
     for (int s = 0; s < Q / 32 * (NT / MH); ++s) {
-      if (s + 1 < Q / 32 * (NT / MH)) load_b(s + 1);
-      stage();
-      mma_cols<MH>(S + s % (NT / MH) * MH, bf[s & 1], xw[s / (NT / MH)]);
+      load_b(s);
+      mma_cols<MH>(S + s % (NT / MH) * MH, bf, xw[s / (NT / MH)]);
     }
   }
   float* to = seg + 1 == L.segments ? A.s_out : nullptr;

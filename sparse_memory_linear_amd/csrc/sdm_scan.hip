@@ -88,7 +88,6 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   const uint32_t xstep = (uint32_t)(XS * A.ld_x) * ES, bstep = (uint32_t)(KS * A.ld_b) * ES,
                  cstep = (uint32_t)(KS * A.ld_c) * ES;
   uint4 rx[NX], rb[NKV], rc[NKV];
-  const bool wide = p0 + kPB <= P && N == NK * 32;  // every column of the tiles is there
   // the next block's rows, on by a block after each fetch
   const long long row0 = (long long)b * A.T + (long long)c0 * Q;
   const char* px = (const char*)A.x + (row0 * A.ld_x + h * P + p0) * ES;
@@ -120,14 +119,14 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   const long long gate0 = bh * R.stride + (long long)c0 * Q;
   const double* gl = R.l + gate0;
   const float *gstep = R.step + gate0, *gfac = (wave == 2 ? R.since : R.left) + gate0;
-  auto fetch_gates = [&] {
+  auto fetch_gates = [&](int on) {  // `on` tokens further than the last time
+    gl += on;
+    gstep += on;
+    gfac += on;
     const int at = lane & (Q - 1);
     rl = gl[at];
     rstep = gstep[at];
     rfac = gfac[at];
-    gl += Q;
-    gstep += Q;
-    gfac += Q;
   };
   auto put_gates = [&] {
     if (lane < Q) {
@@ -184,16 +183,17 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
   // the tiles of M right of the diagonal stay 0
   for (int i = tid; i < 3 * nM / 8; i += 256) ((uint4*)Ms)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (tid == 0) bad_[c0 & 1] = 0;
-  if (c0 < c1) fetch_gates();
+  if (c0 < c1) fetch_gates(0);
   fetch(min(max(n - c0 * Q, 0), Q), 0, 1);
   advance();
-  float* orow = A.o + (bh * A.T + (long long)c0 * Q) * P + p0;
+  float* orow = A.o + (bh * A.T + (long long)c0 * Q) * P;
+  const uint32_t ooff = p0 + 16 * wave + 4 * lg < P ? (uint32_t)(lr * P + p0 + 16 * wave + 4 * lg) * 4 : kNowhere;
   for (int c = c0; c < c1; ++c, orow += Q * P) {
-    const int left = n - c * Q, here = min(max(left, 0), Q), next = min(max(left - Q, 0), Q), rows = min(A.T - c * Q, Q);
+    const int left = n - c * Q, here = min(max(left, 0), Q), next = c + 1 < c1 ? min(max(left - Q, 0), Q) : 0, rows = min(A.T - c * Q, Q);
     if (here == 0) {  // behind the sequence's end, like every block after it
         for (int i = tid; i < rows * (kPB / 4); i += 256) {
           const int k = (i % (kPB / 4)) * 4;
-          if (p0 + k < P) *(float4*)(orow + (long long)(i / (kPB / 4)) * P + k) = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (p0 + k < P) *(float4*)(orow + (long long)(i / (kPB / 4)) * P + p0 + k) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
       continue;
     }
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
     if ((most[1] >= 0x7F80 || (BF16 && most[0] >= 0x7F80))) bad_[c & 1] = 1;
     put_gates();
     const double end = read_lane(rl, Q - 1);
-    if (c + 1 < c1) fetch_gates();
+    fetch_gates(c + 1 < c1 ? Q : 0);
     __syncthreads();
     // x of this wave's channels, tokens along k; and weighted for the state at the block's end
     const float keep = exp2_of(end);
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
       if (k + 1 < NK) load_c(k + 1);
-      if (c + 1 < c1) fetch(next, k, NK);
+      fetch(next, k, NK);
       stage();
       if (k + 1 < NK) split_s(k + 1);
       mma_rows<QT>(Y, Sf[k & 1], cf[k & 1]);
@@ -357,16 +357,10 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
           }
         }
     }
-    float* oo = orow + (long long)lr * P + 16 * wave + 4 * lg;
-    if (wide && here == Q) {
+    const rsrc_t to = block_rows(orow, (uint32_t)(rows * P) * 4);
 #pragma unroll
-      for (int it = 0; it < QT; ++it) *(f32x4_t*)(oo + 16 * it * P) = Y[it];
-    } else if (p0 + 16 * wave + 4 * lg < P) {
-#pragma unroll
-      for (int it = 0; it < QT; ++it)
-        if (16 * it + lr < rows)
-          *(f32x4_t*)(oo + 16 * it * P) = 16 * it + lr < here ? Y[it] : f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int it = 0; it < QT; ++it)
+      store16(to, ooff + (uint32_t)(16 * it * P) * 4, 16 * it + lr < here ? Y[it] : f32x4_t{0.f, 0.f, 0.f, 0.f});
     // the state at the block's end
     constexpr int MH = NT < 4 ? NT : 4;  // tiles of d_k at a time
     Frag<NP> bf[MH];

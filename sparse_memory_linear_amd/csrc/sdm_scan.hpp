@@ -32,8 +32,10 @@ __device__ __forceinline__ float softplus(float x) { return x > 20.f ? x : log1p
 
 __device__ __forceinline__ float exp2_of(double x) { return __builtin_amdgcn_exp2f((float)x); }
 
-// The rows of a block as a buffer: 16 bytes from an offset, zeros from `bytes` on. Rows behind a sequence's
-// end and columns that are not there (kNowhere) so need no branch and no 64-bit address of their own.
+// The rows of a block as a buffer: 16 bytes from an offset, zeros from `bytes` on, where stores are dropped.
+// Rows behind a sequence's end and columns that are not there (kNowhere) so need no branch and no 64-bit
+// address of their own; and a wave waits for its older loads alone, where a branch around newer accesses would
+// have it wait for those too.
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 constexpr uint32_t kNowhere = 0x80000000u;
@@ -43,6 +45,10 @@ __device__ __forceinline__ rsrc_t block_rows(const void* p, uint32_t bytes) {
 __device__ __forceinline__ uint4 load16(rsrc_t rows, uint32_t at) {
   const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(rows, (int)at, 0, 0);
   return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+__device__ __forceinline__ void store16(rsrc_t rows, uint32_t at, f32x4_t v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rows, (int)at, 0, 0);
 }
 
 // High halves of two words as one word (a in the low half)

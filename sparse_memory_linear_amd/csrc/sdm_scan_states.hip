@@ -70,7 +70,9 @@ __global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
   constexpr int XE = XP == 1 ? 8 : 4, KE = KP == 1 ? 8 : 4, XB = XP == 1 ? 2 : 4, KB = KP == 1 ? 2 : 4;
   constexpr int XR = kPB / XE, KR = NK * 32 / KE, NX = Q * XR / 256, NKV = (Q * KR + 255) / 256, XS = 256 / XR, KS = 256 / KR;
   const int xj = tid / XR, xk = (tid % XR) * XE, kj = tid / KR, kk = (tid % KR) * KE;
-  const bool xin = p0 + xk < P, kin = kk < N;
+  const uint32_t xoff = p0 + xk < P ? (uint32_t)(xj * A.ld_x + xk) * XB : kNowhere,
+                 koff = kk < N ? (uint32_t)(kj * A.ld_k + kk) * KB : kNowhere;
+  const uint32_t xstep = (uint32_t)(XS * A.ld_x) * XB, kstep = (uint32_t)(KS * A.ld_k) * KB;
   const char* px0 = (const char*)A.X + ((long long)b * A.xb + (long long)h * A.xh + p0) * XB;
   const char* pk0 = (const char*)A.K + ((long long)b * A.T * A.ld_k + g * N) * KB;
   const float* pw0 = A.weight + bh * A.stride;
@@ -78,22 +80,19 @@ __global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
   // two blocks ahead, in two sets of registers: a block's products are shorter than a load's way
   uint4 rx[2][NX], rk[2][NKV];
   float rw[2] = {0.f, 0.f};
-  double rend[2] = {0.0, 0.0};
+  double rl[2] = {0.0, 0.0};
   auto fetch = [&](int step, int set) {
-    const int c = BACK ? A.blocks - 1 - step : step, here = min(max(n - c * Q, 0), Q);
-    const char* px = px0 + (long long)c * Q * A.ld_x * XB;
-    const char* pk = pk0 + (long long)c * Q * A.ld_k * KB;
-    const int xrows = xin ? here : 0, krows = kin ? here : 0;
+    // (behind the walk's last block: nothing, but the same loads)
+    const int s = min(step, s1 - 1), c = BACK ? A.blocks - 1 - s : s, here = step < s1 ? min(max(n - c * Q, 0), Q) : 0;
+    const rsrc_t rows_x = block_rows(px0 + (long long)c * Q * A.ld_x * XB, (uint32_t)(here * A.ld_x) * XB),
+                 rows_k = block_rows(pk0 + (long long)c * Q * A.ld_k * KB, (uint32_t)(here * A.ld_k) * KB);
 #pragma unroll
-    for (int i = 0; i < NX; ++i)
-      rx[set][i] = xj + i * XS < xrows ? *(const uint4*)(px + ((long long)(xj + i * XS) * A.ld_x + xk) * XB)
-                                  : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < NX; ++i) rx[set][i] = load16(rows_x, xoff + i * xstep);
 #pragma unroll
-    for (int i = 0; i < NKV; ++i)
-      rk[set][i] = kj + i * KS < krows ? *(const uint4*)(pk + ((long long)(kj + i * KS) * A.ld_k + kk) * KB)
-                                  : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < NKV; ++i) rk[set][i] = load16(rows_k, koff + i * kstep);
     rw[set] = pw0[c * Q + (lane & (Q - 1))];
-    rend[set] = pl0[c * Q + Q - 1];
+    // (every lane its own: a scalar load's return would be waited for with the next read of LDS)
+    rl[set] = pl0[c * Q + (lane & (Q - 1))];
   };
   auto put = [&](uint16_t* tile, int plane, int at, const uint4& v, bool whole) {
     if (whole) {
@@ -134,10 +133,11 @@ __global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
     const int c = BACK ? A.blocks - 1 - step : step;
     if (BLOCKS) {
       float* to = A.states + (bh * A.blocks + c) * P * N;
+      const rsrc_t all = block_rows(to, (uint32_t)(P * N) * 4);
 #pragma unroll
       for (int m = 0; m < NT; ++m) {
         const int at = place(m);
-        if (at >= 0) *(f32x4_t*)(to + at) = S[m];
+        store16(all, at >= 0 ? (uint32_t)at * 4 : kNowhere, S[m]);
       }
     }
     __syncthreads();  // the tiles of the block before are read
@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
     for (int i = 0; i < NKV; ++i)
       if (Q * KR % 256 == 0 || kj + i * KS < Q) put(Ks, nK, (kj + i * KS) * LK + kk, rk[set][i], KP == 1);
     if (wave == 0 && lane < Q) w_[lane] = rw[set];
-    const double end = rend[set];
-    if (step + 2 < s1) fetch(step + 2, set);
+    const double end = read_lane(rl[set], Q - 1);
+    fetch(step + 2, set);
     __syncthreads();
     const float keep = exp2_of(end);
     total += end;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
     }
   };
   if (s0 < s1) fetch(s0, 0);
-  if (s0 + 1 < s1) fetch(s0 + 1, 1);
+  if (s0 < s1) fetch(s0 + 1, 1);
   for (int step = s0; step < s1; step += 2) {
     block(step, 0);
     if (step + 1 < s1) block(step + 1, 1);

@@ -264,11 +264,12 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
 #pragma unroll
       for (int e = 0; e < MW; ++e) mma(G[e], gb[k & 1][e], gc[k & 1][e]);
     }
-#pragma unroll
-    for (int e = 0; e < MW; ++e) {
+    auto put_m = [&](int e) {  // tile e of this wave: decays, steps, three pieces
       const int i = 16 * it_[e] + lr, j = 16 * jt_[e] + 4 * lg;
       float mv[4];
-      if (it_[e] != jt_[e]) {
+      // (four token tiles: every wave's first is on the diagonal, its others are not)
+      const bool diagonal = QT == 4 ? e == 0 : it_[e] == jt_[e];
+      if (!diagonal) {
         const float up = up_[i];
         const f32x4_t down = *(const f32x4_t*)(down_[it_[e]] + j);
 #pragma unroll
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
 #pragma unroll
       for (int k = 0; k < 3; ++k)
         *(uint2*)(Ms + k * nM + i * LM + across_order(j)) = make_uint2(w0[k], w1[k]);
-    }
+    };
     f32x4_t Y[QT];
     Frag<NP> cf[2][QT];
     auto load_c = [&](int k) {
@@ -311,18 +312,22 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
       S[2 * k + 1] *= keep;
     };
     split_s(0);
-    __syncthreads();
-    const bool bad = bad_[c & 1] != 0;
+    // the vector work on M and on the state's pieces runs beside the products of C and the state
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
       if (k + 1 < NK) load_c(k + 1);
       fetch(next, k, NK);
       stage();
       if (k + 1 < NK) split_s(k + 1);
+      if (k < MW) put_m(k);
       mma_rows<QT>(Y, Sf[k & 1], cf[k & 1]);
-      interleave<QT * 3 * (NP == 1 ? 1 : 2), NP == 1 ? 5 : 3>();
+      interleave<QT * 3 * (NP == 1 ? 1 : 2), NP == 1 ? 10 : 5>();
       stage();
     }
+#pragma unroll
+    for (int e = NK; e < MW; ++e) put_m(e);
+    __syncthreads();
+    const bool bad = bad_[c & 1] != 0;
     advance();
 #pragma unroll
     for (int it = 0; it < QT; ++it) Y[it] *= since_[16 * it + lr];

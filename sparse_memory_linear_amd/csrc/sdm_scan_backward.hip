@@ -68,7 +68,16 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
   id /= A.G;
   const int blk = id % W.blocks, b = id / W.blocks;
   const int hpg = A.H / A.G, h0 = g * hpg + part * W.heads, h1 = min(h0 + W.heads, (g + 1) * hpg);
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lg = lane >> 4, lr = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int tid = threadIdx.x, lane = tid & 63, lg = lane >> 4, lr = lane & 15;
+  // Where a stage begins: its addresses are made from the thread's index anew. Kept over the loops they would
+  // not fit the registers, and a reload of one waits for every load and store under way.
+  auto anew = [&] {
+    asm volatile("" : "+v"(tid));
+    lane = tid & 63;
+    lg = lane >> 4;
+    lr = lane & 15;
+  };
   const int N = A.N, P = A.P, t0 = blk * Q, n = sequence_length(A.lengths, b, A.T);
   const int here = min(max(n - t0, 0), Q), rows = min(A.T - t0, Q);
   const long long row0 = (long long)b * A.T + t0;
@@ -154,15 +163,17 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
   constexpr int UR = NK * 32 / 4, UN = kPB * UR / kThreads;
   uint4 rx[XN], rg[GN];
   auto fetch = [&](int h, int p0) {  // x and go of a head's channel block
+    const rsrc_t rows_x = block_rows((const char*)A.x + (row0 * A.ld_x + h * P + p0) * ES, (uint32_t)(here * A.ld_x) * ES);
+    const rsrc_t rows_g = block_rows(A.go + (((long long)b * A.H + h) * A.T + t0) * P + p0, (uint32_t)(here * P) * 4);
 #pragma unroll
     for (int i = 0; i < XN; ++i) {
       const int q = tid + kThreads * i, j = q / XR, k = q % XR * E;
-      rx[i] = j < here && p0 + k < P ? *(const uint4*)((const char*)A.x + ((row0 + j) * A.ld_x + h * P + p0 + k) * ES) : zero;
+      rx[i] = load16(rows_x, p0 + k < P ? (uint32_t)(j * A.ld_x + k) * ES : kNowhere);
     }
 #pragma unroll
     for (int i = 0; i < GN; ++i) {
       const int q = tid + kThreads * i, j = q / GR, k = q % GR * 4;
-      rg[i] = j < here && p0 + k < P ? *(const uint4*)(A.go + (((long long)b * A.H + h) * A.T + t0 + j) * P + p0 + k) : zero;
+      rg[i] = load16(rows_g, p0 + k < P ? (uint32_t)(j * P + k) * 4 : kNowhere);
     }
   };
   auto put_xg = [&] {
@@ -178,18 +189,22 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
     }
   };
 
+  // Each tile of x and go is fetched as the one before it goes into LDS: of several channel blocks up for P,
+  // down again for the rest, then the next head's first
+  const int plast = (pblocks - 1) * kPB;
   fetch(h0, 0);
   for (int h = h0; h < h1; ++h) {
+    anew();
     const long long bh = (long long)b * A.H + h;
     const float D = A.D ? A.D[h] : 0.f;
-    const float* S = W.S + (bh * W.blocks + blk) * P * N;
-    const float* U = W.U + (bh * W.blocks + blk) * P * N;
+    const rsrc_t rows_s = block_rows(W.S + (bh * W.blocks + blk) * P * N, (uint32_t)(P * N) * 4);
+    const rsrc_t rows_u = block_rows(W.U + (bh * W.blocks + blk) * P * N, (uint32_t)(P * N) * 4);
     // ---- gates, by every wave in its lanes, one of them each into LDS
     const long long gate = bh * R.stride + t0 + (lane & (Q - 1));
     const double l = R.l[gate];
     const float step = R.step[gate];
+    const float raw = lane < here ? A.dt[(row0 + lane) * A.ld_dt + h] + A.dt_bias[h] : 0.f;
     const double end = read_lane(l, Q - 1);
-    __syncthreads();  // the head before is done
     if (lane < Q) {
       if (wave == 0) l_[lane] = l;
       if (wave == 1) step_[lane] = step;
@@ -213,11 +228,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
 #pragma unroll
     for (int e = 0; e < MW; ++e) Pm[e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     for (int pb = 0; pb < pblocks; ++pb) {
-      if (pb > 0) {
-        fetch(h, pb * kPB);
-        __syncthreads();  // the block before is read
-      }
+      if (pb > 0) __syncthreads();  // the block before is read
       put_xg();
+      if (pb + 1 < pblocks) fetch(h, (pb + 1) * kPB);
+      else if (pblocks > 1) fetch(h, plast - kPB);
+      else if (h + 1 < h1) fetch(h + 1, 0);
       __syncthreads();
 #pragma unroll
       for (int e = 0; e < MW; ++e)
@@ -228,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
         }
     }
 
+    anew();
     // ---- M and R (R's columns in the order of across()), sums over rows and columns of F
 #pragma unroll
     for (int e = 0; e < MW; ++e) {
@@ -297,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
     }
     __syncthreads();
 
+    anew();
     // ---- inside the block: dC, dB; dx of every channel block, the one in LDS first
     if (owns) {
 #pragma unroll
@@ -317,14 +334,16 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
     double us = 0.0;
     for (int q = 0; q < pblocks; ++q) {
       const int pb = pblocks - 1 - q, p0 = pb * kPB;
+      anew();
       f32x4_t dx[JW], du[JW];
 #pragma unroll
       for (int r = 0; r < JW; ++r) dx[r] = du[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       if (q > 0) {
         // (several channel blocks) M's place holds U of the block before: form it again from the registers
-        fetch(h, p0);
         __syncthreads();
         put_xg();
+        if (pb > 0) fetch(h, p0 - kPB);
+        else if (h + 1 < h1) fetch(h + 1, 0);
 #pragma unroll
         for (int e = 0; e < MW; ++e) {
           const int t = wave + kWaves * e;
@@ -350,6 +369,20 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
         }
         __syncthreads();
       }
+      // U of the channel block, and S^T for the states' share: d_k of this lane, 8 channels a step
+      uint4 ru[UN], rs[kPB / 32][2];
+#pragma unroll
+      for (int i = 0; i < UN; ++i) {
+        const int v = tid + kThreads * i, p = v / UR, k = v % UR * 4;
+        ru[i] = load16(rows_u, p0 + p < P && k < N ? (uint32_t)((p0 + p) * N + k) * 4 : kNowhere);
+      }
+#pragma unroll
+      for (int k = 0; k < kPB / 32; ++k) {
+        const int p = p0 + 32 * k + 8 * lg, kk = 16 * nt + lr;
+        const uint32_t at = p < P && kk < N ? (uint32_t)(kk * P + p) * 4 : kNowhere;
+        rs[k][0] = load16(rows_s, at);
+        rs[k][1] = load16(rows_s, at + 16);
+      }
 #pragma unroll
       for (int r = 0; r < JW; ++r)
 #pragma unroll
@@ -357,14 +390,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
           if (k >= (jx + r) / 2)
             mma(dx[r], across<3, 8>(Gs + 32 * k * LX + 32 * (pt >> 1) + 4 * (pt & 1), LX, nX, lane),
                 across<3>(Ms + 32 * k * LM + 16 * (jx + r), LM, nM, lane));
-      // U of the channel block, its rows in the order in which across() takes them
-      uint4 ru[UN];
-#pragma unroll
-      for (int i = 0; i < UN; ++i) {
-        const int v = tid + kThreads * i, p = v / UR, k = v % UR * 4;
-        ru[i] = p0 + p < P && k < N ? *(const uint4*)(U + (long long)(p0 + p) * N + k) : zero;
-      }
       __syncthreads();  // M and R are read
+      // (U's rows in the order in which across() takes them)
 #pragma unroll
       for (int i = 0; i < UN; ++i) {
         const int v = tid + kThreads * i, p = v / UR, k = v % UR * 4;
@@ -381,10 +408,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
       if (owns) {
 #pragma unroll
         for (int k = 0; k < kPB / 32; ++k) {
-          // S^T: d_k of this lane, 8 channels; and the same of U
-          float sv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          const int p = p0 + 32 * k + 8 * lg, kk = 16 * nt + lr;
-          if (p < P && kk < N) load8<false>(S, (long long)kk * P + p, sv);
+          const uint4 s0 = rs[k][0], s1 = rs[k][1];
+          const float sv[8] = {__uint_as_float(s0.x), __uint_as_float(s0.y), __uint_as_float(s0.z), __uint_as_float(s0.w),
+                               __uint_as_float(s1.x), __uint_as_float(s1.y), __uint_as_float(s1.z), __uint_as_float(s1.w)};
           const Frag<3> sf = split8(sv), uf = across<3>(Us + 32 * k * LU + 16 * nt, LU, nU, lane);
           if (wave < NT) {
             float uv[8];
@@ -407,8 +433,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
           *(f32x4_t*)(A.dx + (row0 + j) * A.ld_x + h * P + pp) = j < here ? dx[r] + du[r] * left_[j] : f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
     }
-    if (h + 1 < h1) fetch(h + 1, 0);
-
+    anew();
     // ---- the states' shares of dC and dB, and of the decays' gradients
     if (owns) {
 #pragma unroll
@@ -432,27 +457,28 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
         }
       }
     }
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) us += __shfl_xor(us, m, 64);
-    if (lane == 0) us_[wave] = us;
+    us = block_prefix<64>(us);
+    if (lane == 63) us_[wave] = us;
     __syncthreads();
 
     // ---- time steps: one token per lane of wave 0
     if (wave == 0) {
-      const int i = lane & (Q - 1);
+      anew();
+      const int i = lane & (Q - 1), own = i / 16;
       double row = 0.0, col = 0.0, rd = 0.0, pu = 0.0, whole = 0.0;
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        int it = 1, jt = t - QT;
-        while (jt >= it) jt -= it++;
-        if (t < QT) it = jt = t;
-        row += i / 16 == it ? row_[t][i & 15] : 0.0;
-        col += i / 16 == jt ? col_[t][i & 15] : 0.0;
+      for (int u = 0; u < QT; ++u) {  // tiles of the token's row, and of its column
+        const int lo = min(own, u), hi = max(own, u), t = lo == hi ? own : QT + hi * (hi - 1) / 2 + lo;
+        const double a = row_[t][i & 15], c = col_[t][i & 15];
+        row += u <= own ? a : 0.0;
+        col += u >= own ? c : 0.0;
       }
+#pragma unroll
       for (int k = 0; k < NT; ++k) {
         rd += (double)read_[k][i];
         pu += (double)put_[k][i];
       }
+#pragma unroll
       for (int k = 0; k < kWaves; ++k) whole += us_[k];
       const bool in = lane < here;
       const float rate = -expf(A.A_log[h]);
@@ -462,7 +488,6 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
       const double dl = read_lane(pa, 63) - pa + ahead + pp - behind + (double)exp2_of(end) * whole;
       double ddt = 0.0, da = 0.0, tr = 0.0;
       if (in) {
-        const float raw = A.dt[(row0 + lane) * A.ld_dt + h] + A.dt_bias[h];
         ddt = ((double)diag_[i] + col + pu + dl * (double)rate) * (double)(1.f / (1.f + expf(-raw)));
         da = dl * (double)rate * st;
         tr = (double)trace_[i];

@@ -468,7 +468,7 @@ hipError_t launch_blocks(const ScanArgs& A, const ScanPlan& L, const ScanGates& 
     K.start = A.s_in;
     K.first = W.first;
     K.decay = W.decay;
-    e = launch_scan_walk(K, BF16, false, stream);
+    e = launch_scan_walk(K, BF16, stream);
     if (e != hipSuccess) return e;
   }
   constexpr int lds = Tiles<BF16, NK>::bytes;

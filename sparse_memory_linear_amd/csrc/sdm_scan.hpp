@@ -261,6 +261,9 @@ inline int scan_segments(long long units, int blocks, int wanted) {
   if (s > blocks / 4) s = blocks / 4;
   return s < 1 ? 1 : (int)s;
 }
-hipError_t launch_scan_walk(const ScanWalk& A, bool bf16, bool back, hipStream_t stream);
+// `first` of a forward call's segments, of which there are more than one
+hipError_t launch_scan_walk(const ScanWalk& A, bool bf16, hipStream_t stream);
+// The states of a forward walk A and, with the same sizes, of a walk back U, blocks of each
+hipError_t launch_scan_walks(const ScanWalk& A, const ScanWalk& U, bool bf16, hipStream_t stream);
 
 }  // namespace sdm

@@ -512,10 +512,30 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
   }
 }
 
-// dC and dB from the parts of a group's heads, in their order
-__global__ void __launch_bounds__(256) scan_parts_kernel(ScanArgs A, ScanBwd W) {
+// Workgroups 0 .. H-1: a head's sums over sequences and blocks. The others: dC and dB from the parts of a
+// group's heads. All in their order.
+__global__ void __launch_bounds__(256) scan_finish_kernel(ScanArgs A, ScanBwd W) {
+  if ((int)blockIdx.x < A.H) {
+    __shared__ double part[4][3];
+    const int h = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    double s[3] = {};
+    for (long long i = threadIdx.x; i < (long long)A.B * W.blocks; i += 256)
+      for (int k = 0; k < 3; ++k) s[k] += W.sums[(i * A.H + h) * 3 + k];
+    for (int k = 0; k < 3; ++k) {
+      s[k] = block_prefix<64>(s[k]);
+      if (lane == 63) part[wave][k] = s[k];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int k = 0; k < 3; ++k) s[k] = (part[0][k] + part[1][k]) + (part[2][k] + part[3][k]);
+      A.dA_log[h] = (float)s[0];
+      A.ddt_bias[h] = (float)s[1];
+      if (A.dD) A.dD[h] = (float)s[2];
+    }
+    return;
+  }
   const int per = A.G * A.N / 4;
-  const long long tokens = (long long)A.B * A.T, i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long tokens = (long long)A.B * A.T, i = (long long)(blockIdx.x - A.H) * 256 + threadIdx.x;
   if (i >= 2 * tokens * per) return;
   const int what = (int)(i / (tokens * per));
   const long long at = i % (tokens * per), row = at / per;
@@ -526,39 +546,32 @@ __global__ void __launch_bounds__(256) scan_parts_kernel(ScanArgs A, ScanBwd W) 
   *(f32x4_t*)((what ? A.dBm + row * A.ld_b : A.dCm + row * A.ld_c) + k) = s;
 }
 
-// Sums over sequences and blocks, in their order
-__global__ void __launch_bounds__(64) scan_sum_kernel(ScanArgs A, ScanBwd W) {
-  const int h = blockIdx.x, lane = threadIdx.x;
-  double s[3] = {};
-  for (long long i = lane; i < (long long)A.B * W.blocks; i += 64)
-    for (int k = 0; k < 3; ++k) s[k] += W.sums[(i * A.H + h) * 3 + k];
-  for (int m = 32; m >= 1; m >>= 1)
-    for (int k = 0; k < 3; ++k) s[k] += __shfl_xor(s[k], m, 64);
-  if (lane == 0) {
-    A.dA_log[h] = (float)s[0];
-    A.ddt_bias[h] = (float)s[1];
-    if (A.dD) A.dD[h] = (float)s[2];
-  }
-}
-
 struct BwdPlan {
   ScanGates gates;
   ScanBwd bwd;
   int segments;
-  float* first;
-  double* decay;
+  float *first, *first_back;
+  double *decay, *decay_back;
   size_t bytes;
 };
 
-// A group's heads are shared out over workgroups until about two per compute unit are there.
+// A group's heads are shared out over workgroups, one of which fills a compute unit: for the fewest rounds of
+// 256 times a workgroup's length, in which the products of B and C count as half a head.
 BwdPlan plan_of(const sdm_scan_shape& S, char* base) {
   BwdPlan L{};
   const int Q = S.in_dtype == SDM_BF16 ? 64 : 32, hpg = S.H / S.G;
   const size_t units = (size_t)S.B * S.H, state = (size_t)S.d_v * S.d_k * 4;
   L.bwd.blocks = (S.T + Q - 1) / Q;
   const long long groups = (long long)S.B * S.G * L.bwd.blocks;
-  long long parts = groups > 0 ? (512 + groups - 1) / groups : 1;
-  if (parts > hpg) parts = hpg;
+  long long parts = 1;
+  double best = 0.0;
+  for (int p = 1; p <= hpg && p <= 512; ++p) {
+    const double cost = (double)((groups * p + 255) / 256) * ((hpg + p - 1) / p + 0.5);
+    if (p == 1 || cost < best) {
+      parts = p;
+      best = cost;
+    }
+  }
   L.bwd.heads = (int)((hpg + parts - 1) / parts);
   L.bwd.parts = (hpg + L.bwd.heads - 1) / L.bwd.heads;
   L.segments = scan_segments((long long)units * ((S.d_v + kPB - 1) / kPB), L.bwd.blocks, 768);
@@ -576,7 +589,11 @@ BwdPlan plan_of(const sdm_scan_shape& S, char* base) {
   if (L.segments > 1) {
     L.first = (float*)(base + at);
     at += align_up(units * L.segments * state);
+    L.first_back = (float*)(base + at);
+    at += align_up(units * L.segments * state);
     L.decay = (double*)(base + at);
+    at += align_up(units * L.segments * 8);
+    L.decay_back = (double*)(base + at);
     at += align_up(units * L.segments * 8);
   }
   L.bytes = at + 256;  // (never empty)
@@ -622,19 +639,22 @@ hipError_t launch_scan_backward(const sdm_scan_shape& S, const ScanArgs& A, hipS
   K.weight = L.gates.left;
   K.start = A.s_in;
   K.states = (float*)L.bwd.S;
-  e = launch_scan_walk(K, A.bf16, false, stream);
-  if (e != hipSuccess) return e;
-  K.X = A.go;
-  K.K = A.Cm;
-  K.xb = (long long)A.H * A.T * A.P;
-  K.xh = (long long)A.T * A.P;
-  K.ld_x = A.P;
-  K.ld_k = A.ld_c;
-  K.weight = L.gates.since;
-  K.start = A.ds_out;
-  K.end = A.ds_in;
-  K.states = (float*)L.bwd.U;
-  e = launch_scan_walk(K, A.bf16, true, stream);
+  ScanWalk U = K;  // and back, for the states' gradients
+  U.X = A.go;
+  U.K = A.Cm;
+  U.xb = (long long)A.H * A.T * A.P;
+  U.xh = (long long)A.T * A.P;
+  U.ld_x = A.P;
+  U.ld_k = A.ld_c;
+  U.weight = L.gates.since;
+  U.start = A.ds_out;
+  U.end = A.ds_in;
+  U.states = (float*)L.bwd.U;
+  if (L.segments > 1) {
+    U.first = L.first_back;
+    U.decay = L.decay_back;
+  }
+  e = launch_scan_walks(K, U, A.bf16, stream);
   if (e != hipSuccess) return e;
   if (L.bwd.blocks > 0) {
     e = A.bf16   ? (A.N <= 32   ? launch_main<true, 1>(A, L, stream)
@@ -644,14 +664,9 @@ hipError_t launch_scan_backward(const sdm_scan_shape& S, const ScanArgs& A, hipS
         : A.N <= 64 ? launch_main<false, 2>(A, L, stream)
                     : launch_main<false, 4>(A, L, stream);
     if (e != hipSuccess) return e;
-    if (L.bwd.parts > 1) {
-      const long long quads = 2ll * A.B * A.T * (A.G * A.N / 4);
-      hipLaunchKernelGGL(scan_parts_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, A, L.bwd);
-      e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
   }
-  hipLaunchKernelGGL(scan_sum_kernel, dim3(A.H), dim3(64), 0, stream, A, L.bwd);
+  const long long quads = L.bwd.blocks > 0 && L.bwd.parts > 1 ? 2ll * A.B * A.T * (A.G * A.N / 4) : 0;
+  hipLaunchKernelGGL(scan_finish_kernel, dim3((unsigned)(A.H + (quads + 255) / 256)), dim3(256), 0, stream, A, L.bwd);
   return hipGetLastError();
 }
 

@@ -50,15 +50,13 @@ __global__ void __launch_bounds__(256) scan_gates_kernel(ScanArgs A, ScanGates g
 constexpr int kPB = 64;
 
 template <int XP, int KP, int NK, bool BACK, bool BLOCKS, bool TURN>
-__global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
+__device__ __forceinline__ void walk(const ScanWalk& A, int id, uint16_t* lds, float* w_) {
   constexpr int Q = KP == 1 ? 64 : 32, NT = 2 * NK;
   constexpr int LX = kPB + 16, LK = NK * 32 + 16, nX = Q * LX, nK = Q * LK;
-  extern __shared__ __align__(16) uint16_t lds[];
-  __shared__ __align__(16) float w_[Q];
   uint16_t *Ks = lds, *Xs = Ks + KP * nK;
 
   const int fast = A.B * A.G * A.segs, hpg = A.H / A.G;
-  const int f = blockIdx.x % fast, s = blockIdx.x / fast;
+  const int f = id % fast, s = id / fast;
   const int seg = f / (A.B * A.G), b = f % (A.B * A.G) / A.G, g = f % A.G;
   const int h = g * hpg + s % hpg, pb = s / hpg, p0 = pb * kPB;
   const long long bh = (long long)b * A.H + h;
@@ -195,11 +193,29 @@ __global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
   if (!BLOCKS && tid == 0 && pb == 0) A.decay[(long long)(seg + 1) * A.B * A.H + bh] = total;
 }
 
+// The walk for the first states of the forward pass's segments
+template <int KP, int NK>
+__global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
+  extern __shared__ __align__(16) uint16_t lds[];
+  __shared__ __align__(16) float w_[64];
+  walk<KP, KP, NK, false, false, false>(A, blockIdx.x, lds, w_);
+}
+
+// The gradient's two walks, which need nothing of each other: workgroups of the longer one, back, come first
+template <int KP, int NK, bool BLOCKS>
+__global__ void __launch_bounds__(256, 2) scan_walks_kernel(ScanWalk A, ScanWalk U) {
+  extern __shared__ __align__(16) uint16_t lds[];
+  __shared__ __align__(16) float w_[64];
+  const int half = gridDim.x / 2;
+  if ((int)blockIdx.x < half) walk<3, KP, NK, true, BLOCKS, false>(U, blockIdx.x, lds, w_);
+  else walk<KP, KP, NK, false, BLOCKS, true>(A, blockIdx.x - half, lds, w_);
+}
+
 // States before the segments, from the segments' own ends: first[0] is the call's first state, first[s]
 // (which holds what segment s-1 adds) takes up first[s-1] decayed over segment s-1. `turned`: of [d_k][d_v].
-__global__ void __launch_bounds__(256) scan_join_kernel(ScanWalk A, bool turned) {
+__device__ __forceinline__ void join(const ScanWalk& A, bool turned, long long group) {
   const long long per = (long long)A.P * A.N / 4, units = (long long)A.B * A.H;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long i = group * 256 + threadIdx.x;
   if (i >= units * per) return;
   f32x4_t* v = (f32x4_t*)A.first;
   f32x4_t s = {0.f, 0.f, 0.f, 0.f};
@@ -227,26 +243,43 @@ __global__ void __launch_bounds__(256) scan_join_kernel(ScanWalk A, bool turned)
   }
 }
 
-template <int XP, int KP, int NK, bool BACK, bool BLOCKS, bool TURN>
-hipError_t launch_walk_kernel(ScanWalk A, hipStream_t stream) {
-  constexpr int Q = KP == 1 ? 64 : 32;
-  constexpr int lds = (KP * Q * (NK * 32 + 16) + XP * Q * (kPB + 16)) * 2;
-  A.segs = BLOCKS ? A.segments : A.segments - 1;
-  const long long units = (long long)A.B * A.H * ((A.P + kPB - 1) / kPB) * A.segs;
-  hipLaunchKernelGGL((scan_walk_kernel<XP, KP, NK, BACK, BLOCKS, TURN>), dim3((unsigned)units), dim3(256), lds, stream, A);
+__global__ void __launch_bounds__(256) scan_join_kernel(ScanWalk A) { join(A, false, blockIdx.x); }
+__global__ void __launch_bounds__(256) scan_joins_kernel(ScanWalk A, ScanWalk U) {
+  const int half = gridDim.x / 2;
+  if ((int)blockIdx.x < half) join(A, true, blockIdx.x);
+  else join(U, false, blockIdx.x - half);
+}
+
+unsigned join_groups(const ScanWalk& A) { return (unsigned)(((long long)A.B * A.H * A.P * A.N / 4 + 255) / 256); }
+unsigned walk_groups(const ScanWalk& A) { return (unsigned)((long long)A.B * A.H * ((A.P + kPB - 1) / kPB) * A.segs); }
+constexpr int walk_lds(int XP, int KP, int NK) {
+  return (KP * (KP == 1 ? 64 : 32) * (NK * 32 + 16) + XP * (KP == 1 ? 64 : 32) * (kPB + 16)) * 2;
+}
+
+template <int KP, int NK>
+hipError_t launch_walk(ScanWalk A, hipStream_t stream) {
+  constexpr int lds = walk_lds(KP, KP, NK);
+  A.segs = A.segments - 1;
+  hipLaunchKernelGGL((scan_walk_kernel<KP, NK>), dim3(walk_groups(A)), dim3(256), lds, stream, A);
   return hipGetLastError();
 }
 
-template <bool BACK, bool BLOCKS, bool TURN>
-hipError_t launch_walk(const ScanWalk& A, bool bf16, hipStream_t stream) {
-  constexpr int XP = BACK ? 3 : 1;  // pieces of X beside bf16 inputs: go is float32
+template <int KP, int NK, bool BLOCKS>
+hipError_t launch_walks(ScanWalk A, ScanWalk U, hipStream_t stream) {
+  constexpr int lds = walk_lds(3, KP, NK);  // (go is float32: three pieces)
+  A.segs = U.segs = BLOCKS ? A.segments : A.segments - 1;
+  hipLaunchKernelGGL((scan_walks_kernel<KP, NK, BLOCKS>), dim3(2 * walk_groups(A)), dim3(256), lds, stream, A, U);
+  return hipGetLastError();
+}
+template <bool BLOCKS>
+hipError_t launch_walks_of(const ScanWalk& A, const ScanWalk& U, bool bf16, hipStream_t stream) {
   if (bf16)
-    return A.N <= 32   ? launch_walk_kernel<XP, 1, 1, BACK, BLOCKS, TURN>(A, stream)
-           : A.N <= 64 ? launch_walk_kernel<XP, 1, 2, BACK, BLOCKS, TURN>(A, stream)
-                       : launch_walk_kernel<XP, 1, 4, BACK, BLOCKS, TURN>(A, stream);
-  return A.N <= 32   ? launch_walk_kernel<3, 3, 1, BACK, BLOCKS, TURN>(A, stream)
-         : A.N <= 64 ? launch_walk_kernel<3, 3, 2, BACK, BLOCKS, TURN>(A, stream)
-                     : launch_walk_kernel<3, 3, 4, BACK, BLOCKS, TURN>(A, stream);
+    return A.N <= 32   ? launch_walks<1, 1, BLOCKS>(A, U, stream)
+           : A.N <= 64 ? launch_walks<1, 2, BLOCKS>(A, U, stream)
+                       : launch_walks<1, 4, BLOCKS>(A, U, stream);
+  return A.N <= 32   ? launch_walks<3, 1, BLOCKS>(A, U, stream)
+         : A.N <= 64 ? launch_walks<3, 2, BLOCKS>(A, U, stream)
+                     : launch_walks<3, 4, BLOCKS>(A, U, stream);
 }
 
 }  // namespace
@@ -259,21 +292,27 @@ hipError_t launch_scan_gates(const ScanArgs& A, int Q, const ScanGates& g, hipSt
   return hipGetLastError();
 }
 
-hipError_t launch_scan_walk(const ScanWalk& A, bool bf16, bool back, hipStream_t stream) {
-  const bool turned = A.states && !back;
-  hipError_t e = hipSuccess;
+hipError_t launch_scan_walk(const ScanWalk& A, bool bf16, hipStream_t stream) {
+  hipError_t e = bf16          ? (A.N <= 32   ? launch_walk<1, 1>(A, stream)
+                                  : A.N <= 64 ? launch_walk<1, 2>(A, stream)
+                                              : launch_walk<1, 4>(A, stream))
+                 : A.N <= 32 ? launch_walk<3, 1>(A, stream)
+                 : A.N <= 64 ? launch_walk<3, 2>(A, stream)
+                             : launch_walk<3, 4>(A, stream);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(scan_join_kernel, dim3(join_groups(A)), dim3(256), 0, stream, A);
+  return hipGetLastError();
+}
+
+hipError_t launch_scan_walks(const ScanWalk& A, const ScanWalk& U, bool bf16, hipStream_t stream) {
   if (A.segments > 1) {
-    e = back     ? launch_walk<true, false, false>(A, bf16, stream)
-        : turned ? launch_walk<false, false, true>(A, bf16, stream)
-                 : launch_walk<false, false, false>(A, bf16, stream);
+    hipError_t e = launch_walks_of<false>(A, U, bf16, stream);
     if (e != hipSuccess) return e;
-    const long long quads = (long long)A.B * A.H * A.P * A.N / 4;
-    hipLaunchKernelGGL(scan_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, A, turned);
+    hipLaunchKernelGGL(scan_joins_kernel, dim3(2 * join_groups(A)), dim3(256), 0, stream, A, U);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (!A.states) return e;
-  return back ? launch_walk<true, true, false>(A, bf16, stream) : launch_walk<false, true, true>(A, bf16, stream);
+  return launch_walks_of<true>(A, U, bf16, stream);
 }
 
 }  // namespace sdm

@@ -248,11 +248,13 @@ struct ScanWalk {
   const double* l;
   const float* start;  // state before the walk, or null
   float* end;          // state behind it, or null
-  float* first;        // [segments][B*H][P][N]: states before the segments
-  double* decay;       // [segments][B*H]: log2 of the segments' decay
-  // [B*H][blocks] states entering the blocks, forward [N][P] (as then `first` too), backward [P][N]; null: only
-  // `first` is wanted
-  float* states;
+  // of several segments: [segments + 1][B*H][P][N] states before them (forward with `states`: [N][P]), the last
+  // place for what the last one adds; and [segments + 1][B*H] log2 of the decay of the segment before
+  float* first;
+  double* decay;
+  // [B*H][blocks] what the segment adds to the states entering the blocks, forward [N][P], backward [P][N], and
+  // [B*H][blocks] the decay from the segment's start to there; null: only `first` is wanted
+  float *states, *upto;
 };
 // Segments of a walk (or of the forward kernel): a call of few units is split until `wanted` workgroups are
 // busy, each with at least four blocks, so that enough share the pass that finds the segments' first states.

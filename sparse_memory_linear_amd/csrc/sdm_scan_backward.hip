@@ -32,8 +32,11 @@ constexpr int kPB = 64;       // channels per tile
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 
 struct ScanBwd {
-  const float* S;  // [B*H][blocks][N][P]
-  const float* U;  // [B*H][blocks][P][N]
+  // The states before the blocks and the gradients behind them, in segments of blocks: what the segment adds,
+  // [B*H][blocks] of [N][P] and of [P][N], and, of several segments, the states before those,
+  // [segments][B*H], and the factors they take for the block, [B*H][blocks]
+  const float *S, *U, *S_first, *U_first, *S_upto, *U_upto;
+  int segments;
   double* sums;    // [B*blocks][H][3]: dA_log, ddt_bias, dD of the block
   float* part;     // [parts][2][B*T][G*N]: dC and dB of the parts' heads (parts > 1)
   int blocks, parts, heads;  // heads per part
@@ -189,6 +192,16 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
     }
   };
 
+  // the segments in which the two walks came to this block, and the blocks that those began with
+  const int sseg = (int)(((long long)(blk + 1) * W.segments - 1) / W.blocks), seg_s = (int)((long long)W.blocks * sseg / W.segments);
+  const int useg = (int)(((long long)(W.blocks - blk) * W.segments - 1) / W.blocks),
+            seg_u = W.blocks - 1 - (int)((long long)W.blocks * useg / W.segments);
+  auto joined = [](const uint4& v, const uint4& first, float upto) {
+    return make_uint4(__float_as_uint(fmaf(__uint_as_float(first.x), upto, __uint_as_float(v.x))),
+                      __float_as_uint(fmaf(__uint_as_float(first.y), upto, __uint_as_float(v.y))),
+                      __float_as_uint(fmaf(__uint_as_float(first.z), upto, __uint_as_float(v.z))),
+                      __float_as_uint(fmaf(__uint_as_float(first.w), upto, __uint_as_float(v.w))));
+  };
   // Each tile of x and go is fetched as the one before it goes into LDS: of several channel blocks up for P,
   // down again for the rest, then the next head's first
   const int plast = (pblocks - 1) * kPB;
@@ -197,8 +210,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
     anew();
     const long long bh = (long long)b * A.H + h;
     const float D = A.D ? A.D[h] : 0.f;
-    const rsrc_t rows_s = block_rows(W.S + (bh * W.blocks + blk) * P * N, (uint32_t)(P * N) * 4);
-    const rsrc_t rows_u = block_rows(W.U + (bh * W.blocks + blk) * P * N, (uint32_t)(P * N) * 4);
+    // S and U: what the segment adds (nothing before its first block), and of several segments what was before it
+    const uint32_t state = (uint32_t)(P * N) * 4;
+    const bool split = W.segments > 1;
+    const rsrc_t rows_s = block_rows(W.S + (bh * W.blocks + blk) * P * N, split && blk == seg_s ? 0u : state);
+    const rsrc_t rows_u = block_rows(W.U + (bh * W.blocks + blk) * P * N, split && blk == seg_u ? 0u : state);
+    const rsrc_t rows_sf = block_rows(W.S_first + ((long long)sseg * A.B * A.H + bh) * P * N, split ? state : 0u);
+    const rsrc_t rows_uf = block_rows(W.U_first + ((long long)useg * A.B * A.H + bh) * P * N, split ? state : 0u);
+    const float upto_s = split ? W.S_upto[bh * W.blocks + blk] : 0.f, upto_u = split ? W.U_upto[bh * W.blocks + blk] : 0.f;
     // ---- gates, by every wave in its lanes, one of them each into LDS
     const long long gate = bh * R.stride + t0 + (lane & (Q - 1));
     const double l = R.l[gate];
@@ -370,11 +389,13 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
         __syncthreads();
       }
       // U of the channel block, and S^T for the states' share: d_k of this lane, 8 channels a step
-      uint4 ru[UN], rs[kPB / 32][2];
+      uint4 ru[UN], uf_[UN], rs[kPB / 32][2], sf_[kPB / 32][2];
 #pragma unroll
       for (int i = 0; i < UN; ++i) {
         const int v = tid + kThreads * i, p = v / UR, k = v % UR * 4;
-        ru[i] = load16(rows_u, p0 + p < P && k < N ? (uint32_t)((p0 + p) * N + k) * 4 : kNowhere);
+        const uint32_t at = p0 + p < P && k < N ? (uint32_t)((p0 + p) * N + k) * 4 : kNowhere;
+        ru[i] = load16(rows_u, at);
+        uf_[i] = load16(rows_uf, at);
       }
 #pragma unroll
       for (int k = 0; k < kPB / 32; ++k) {
@@ -382,6 +403,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
         const uint32_t at = p < P && kk < N ? (uint32_t)(kk * P + p) * 4 : kNowhere;
         rs[k][0] = load16(rows_s, at);
         rs[k][1] = load16(rows_s, at + 16);
+        sf_[k][0] = load16(rows_sf, at);
+        sf_[k][1] = load16(rows_sf, at + 16);
       }
 #pragma unroll
       for (int r = 0; r < JW; ++r)
@@ -396,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
       for (int i = 0; i < UN; ++i) {
         const int v = tid + kThreads * i, p = v / UR, k = v % UR * 4;
         const int at = (p & 32) | ((p & 4) << 2) | ((p & 24) >> 1) | (p & 3);
-        put(Us, nU, at * LU + k, ru[i], false);
+        put(Us, nU, at * LU + k, joined(ru[i], uf_[i], upto_u), false);
       }
       __syncthreads();
 #pragma unroll
@@ -408,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
       if (owns) {
 #pragma unroll
         for (int k = 0; k < kPB / 32; ++k) {
-          const uint4 s0 = rs[k][0], s1 = rs[k][1];
+          const uint4 s0 = joined(rs[k][0], sf_[k][0], upto_s), s1 = joined(rs[k][1], sf_[k][1], upto_s);
           const float sv[8] = {__uint_as_float(s0.x), __uint_as_float(s0.y), __uint_as_float(s0.z), __uint_as_float(s0.w),
                                __uint_as_float(s1.x), __uint_as_float(s1.y), __uint_as_float(s1.z), __uint_as_float(s1.w)};
           const Frag<3> sf = split8(sv), uf = across<3>(Us + 32 * k * LU + 16 * nt, LU, nU, lane);
@@ -549,8 +572,6 @@ __global__ void __launch_bounds__(256) scan_finish_kernel(ScanArgs A, ScanBwd W)
 struct BwdPlan {
   ScanGates gates;
   ScanBwd bwd;
-  int segments;
-  float *first, *first_back;
   double *decay, *decay_back;
   size_t bytes;
 };
@@ -574,7 +595,7 @@ BwdPlan plan_of(const sdm_scan_shape& S, char* base) {
   }
   L.bwd.heads = (int)((hpg + parts - 1) / parts);
   L.bwd.parts = (hpg + L.bwd.heads - 1) / L.bwd.heads;
-  L.segments = scan_segments((long long)units * ((S.d_v + kPB - 1) / kPB), L.bwd.blocks, 768);
+  L.bwd.segments = scan_segments((long long)units * ((S.d_v + kPB - 1) / kPB), L.bwd.blocks, 768);
   size_t at = gates_bytes(units, S.T, base, &L.gates);
   L.bwd.S = (float*)(base + at);
   at += align_up(units * L.bwd.blocks * state);
@@ -586,15 +607,17 @@ BwdPlan plan_of(const sdm_scan_shape& S, char* base) {
     L.bwd.part = (float*)(base + at);
     at += align_up((size_t)L.bwd.parts * 2 * S.B * S.T * S.G * S.d_k * 4);
   }
-  if (L.segments > 1) {
-    L.first = (float*)(base + at);
-    at += align_up(units * L.segments * state);
-    L.first_back = (float*)(base + at);
-    at += align_up(units * L.segments * state);
+  if (L.bwd.segments > 1) {
+    const size_t slots = units * (L.bwd.segments + 1), factors = align_up(units * L.bwd.blocks * 4);
+    L.bwd.S_first = (float*)(base + at);
+    L.bwd.U_first = (float*)(base + at + align_up(slots * state));
+    at += 2 * align_up(slots * state);
     L.decay = (double*)(base + at);
-    at += align_up(units * L.segments * 8);
-    L.decay_back = (double*)(base + at);
-    at += align_up(units * L.segments * 8);
+    L.decay_back = (double*)(base + at + align_up(slots * 8));
+    at += 2 * align_up(slots * 8);
+    L.bwd.S_upto = (float*)(base + at);
+    L.bwd.U_upto = (float*)(base + at + factors);
+    at += 2 * factors;
   }
   L.bytes = at + 256;  // (never empty)
   return L;
@@ -624,11 +647,12 @@ hipError_t launch_scan_backward(const sdm_scan_shape& S, const ScanArgs& A, hipS
   K.N = A.N;
   K.P = A.P;
   K.blocks = L.bwd.blocks;
-  K.segments = L.segments;
+  K.segments = L.bwd.segments;
   K.stride = L.gates.stride;
   K.lengths = A.lengths;
   K.l = L.gates.l;
-  K.first = L.first;
+  K.first = (float*)L.bwd.S_first;
+  K.upto = (float*)L.bwd.S_upto;
   K.decay = L.decay;
   K.X = A.x;
   K.K = A.Bm;
@@ -650,10 +674,9 @@ hipError_t launch_scan_backward(const sdm_scan_shape& S, const ScanArgs& A, hipS
   U.start = A.ds_out;
   U.end = A.ds_in;
   U.states = (float*)L.bwd.U;
-  if (L.segments > 1) {
-    U.first = L.first_back;
-    U.decay = L.decay_back;
-  }
+  U.first = (float*)L.bwd.U_first;
+  U.decay = L.decay_back;
+  U.upto = (float*)L.bwd.U_upto;
   e = launch_scan_walks(K, U, A.bf16, stream);
   if (e != hipSuccess) return e;
   if (L.bwd.blocks > 0) {

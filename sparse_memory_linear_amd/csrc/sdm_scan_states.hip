@@ -44,7 +44,11 @@ __global__ void __launch_bounds__(256) scan_gates_kernel(ScanArgs A, ScanGates g
 // 16 w .. 16 w + 15, all d_k. Forward X = x, K = B, w = left; backward, from the last block to the first,
 // X = go, K = C, w = since. A block's loads are in flight while the block before is multiplied.
 //
-// With BLOCKS the state that enters each block is stored (backward: the gradient of the state after it).
+// Segments start at zero. With BLOCKS what the segment adds to the state that enters each of its blocks but the
+// first is stored (backward: to the gradient of the state after it), and the decay up to there, by which the
+// state before the segment, which is known only behind this walk, still has to be multiplied. So one pass over
+// the tokens does: a pass for the segments' ends first took 33 us more (4 x 2048 tokens, 8 heads of 128 x 128).
+// A walk of one segment starts from the call's state and stores all.
 // TURN: results as [channel][d_k] tiles, whose lanes hold 4 consecutive channels, and states as [d_k][d_v]; else
 // the other way round. Each is stored the way the products that read it take it.
 constexpr int kPB = 64;
@@ -110,12 +114,11 @@ __device__ __forceinline__ void walk(const ScanWalk& A, int id, uint16_t* lds, f
     return p < P && k < N ? (TURN ? k * P + p : p * N + k) : -1;
   };
   f32x4_t S[NT];
-  const float* from = A.segments > 1 && BLOCKS ? A.first + ((long long)seg * A.B * A.H + bh) * P * N : nullptr;
   const float* start = A.segments == 1 && A.start ? A.start + bh * P * N : nullptr;
 #pragma unroll
   for (int m = 0; m < NT; ++m) {
     const int at = place(m);
-    S[m] = from && at >= 0 ? *(const f32x4_t*)(from + at) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+    S[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     if (start && at >= 0) {
       if (TURN) {  // [d_v][d_k]
 #pragma unroll
@@ -131,7 +134,9 @@ __device__ __forceinline__ void walk(const ScanWalk& A, int id, uint16_t* lds, f
     const int c = BACK ? A.blocks - 1 - step : step;
     if (BLOCKS) {
       float* to = A.states + (bh * A.blocks + c) * P * N;
-      const rsrc_t all = block_rows(to, (uint32_t)(P * N) * 4);
+      // (nothing of a segment's first block, but the same stores)
+      const rsrc_t all = block_rows(to, A.segments == 1 || step > s0 ? (uint32_t)(P * N) * 4 : 0u);
+      if (A.upto && tid == 0 && pb == 0) A.upto[bh * A.blocks + c] = exp2_of(total);
 #pragma unroll
       for (int m = 0; m < NT; ++m) {
         const int at = place(m);
@@ -180,17 +185,17 @@ __device__ __forceinline__ void walk(const ScanWalk& A, int id, uint16_t* lds, f
     block(step, 0);
     if (step + 1 < s1) block(step + 1, 1);
   }
-  float* to = !BLOCKS                     ? A.first + ((long long)(seg + 1) * A.B * A.H + bh) * P * N
-              : seg + 1 == A.segments && A.end ? A.end + bh * P * N
-                                               : nullptr;
-  if (to) {  // (a turned walk has no end)
+  float* to = A.segments > 1 ? A.first + ((long long)(seg + 1) * A.B * A.H + bh) * P * N
+              : A.end        ? A.end + bh * P * N
+                             : nullptr;
+  if (to) {  // (a turned walk of one segment has no end)
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
       const int at = place(m);
       if (at >= 0) *(f32x4_t*)(to + at) = S[m];
     }
   }
-  if (!BLOCKS && tid == 0 && pb == 0) A.decay[(long long)(seg + 1) * A.B * A.H + bh] = total;
+  if (A.segments > 1 && tid == 0 && pb == 0) A.decay[(long long)(seg + 1) * A.B * A.H + bh] = total;
 }
 
 // The walk for the first states of the forward pass's segments
@@ -202,17 +207,18 @@ __global__ void __launch_bounds__(256, 2) scan_walk_kernel(ScanWalk A) {
 }
 
 // The gradient's two walks, which need nothing of each other: workgroups of the longer one, back, come first
-template <int KP, int NK, bool BLOCKS>
+template <int KP, int NK>
 __global__ void __launch_bounds__(256, 2) scan_walks_kernel(ScanWalk A, ScanWalk U) {
   extern __shared__ __align__(16) uint16_t lds[];
   __shared__ __align__(16) float w_[64];
   const int half = gridDim.x / 2;
-  if ((int)blockIdx.x < half) walk<3, KP, NK, true, BLOCKS, false>(U, blockIdx.x, lds, w_);
-  else walk<KP, KP, NK, false, BLOCKS, true>(A, blockIdx.x - half, lds, w_);
+  if ((int)blockIdx.x < half) walk<3, KP, NK, true, true, false>(U, blockIdx.x, lds, w_);
+  else walk<KP, KP, NK, false, true, true>(A, blockIdx.x - half, lds, w_);
 }
 
 // States before the segments, from the segments' own ends: first[0] is the call's first state, first[s]
-// (which holds what segment s-1 adds) takes up first[s-1] decayed over segment s-1. `turned`: of [d_k][d_v].
+// (which holds what segment s-1 adds) takes up first[s-1] decayed over segment s-1, and so the call's end.
+// `turned`: of [d_k][d_v].
 __device__ __forceinline__ void join(const ScanWalk& A, bool turned, long long group) {
   const long long per = (long long)A.P * A.N / 4, units = (long long)A.B * A.H;
   const long long i = group * 256 + threadIdx.x;
@@ -228,18 +234,23 @@ __device__ __forceinline__ void join(const ScanWalk& A, bool turned, long long g
     s = ((const f32x4_t*)A.start)[i];
   }
   v[i] = s;
-  for (int k0 = 1; k0 < A.segments; k0 += 8) {  // eight loads in flight
+  const int last = A.segments - (A.end ? 0 : 1);
+  for (int k0 = 1; k0 <= last; k0 += 8) {  // eight loads in flight
     f32x4_t add[8];
     float keep[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const long long k = min(k0 + u, A.segments - 1);
+      const long long k = min(k0 + u, last);
       add[u] = v[k * units * per + i];
       keep[u] = exp2_of(A.decay[k * units + i / per]);
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      if (k0 + u < A.segments) v[(k0 + u) * units * per + i] = s = add[u] + s * keep[u];
+      if (k0 + u <= last) {
+        s = add[u] + s * keep[u];
+        if (k0 + u < A.segments) v[(k0 + u) * units * per + i] = s;
+        else ((f32x4_t*)A.end)[i] = s;
+      }
   }
 }
 
@@ -264,24 +275,13 @@ hipError_t launch_walk(ScanWalk A, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int KP, int NK, bool BLOCKS>
+template <int KP, int NK>
 hipError_t launch_walks(ScanWalk A, ScanWalk U, hipStream_t stream) {
   constexpr int lds = walk_lds(3, KP, NK);  // (go is float32: three pieces)
-  A.segs = U.segs = BLOCKS ? A.segments : A.segments - 1;
-  hipLaunchKernelGGL((scan_walks_kernel<KP, NK, BLOCKS>), dim3(2 * walk_groups(A)), dim3(256), lds, stream, A, U);
+  A.segs = U.segs = A.segments;
+  hipLaunchKernelGGL((scan_walks_kernel<KP, NK>), dim3(2 * walk_groups(A)), dim3(256), lds, stream, A, U);
   return hipGetLastError();
 }
-template <bool BLOCKS>
-hipError_t launch_walks_of(const ScanWalk& A, const ScanWalk& U, bool bf16, hipStream_t stream) {
-  if (bf16)
-    return A.N <= 32   ? launch_walks<1, 1, BLOCKS>(A, U, stream)
-           : A.N <= 64 ? launch_walks<1, 2, BLOCKS>(A, U, stream)
-                       : launch_walks<1, 4, BLOCKS>(A, U, stream);
-  return A.N <= 32   ? launch_walks<3, 1, BLOCKS>(A, U, stream)
-         : A.N <= 64 ? launch_walks<3, 2, BLOCKS>(A, U, stream)
-                     : launch_walks<3, 4, BLOCKS>(A, U, stream);
-}
-
 }  // namespace
 
 hipError_t launch_scan_gates(const ScanArgs& A, int Q, const ScanGates& g, hipStream_t stream) {
@@ -305,14 +305,15 @@ hipError_t launch_scan_walk(const ScanWalk& A, bool bf16, hipStream_t stream) {
 }
 
 hipError_t launch_scan_walks(const ScanWalk& A, const ScanWalk& U, bool bf16, hipStream_t stream) {
-  if (A.segments > 1) {
-    hipError_t e = launch_walks_of<false>(A, U, bf16, stream);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(scan_joins_kernel, dim3(2 * join_groups(A)), dim3(256), 0, stream, A, U);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return launch_walks_of<true>(A, U, bf16, stream);
+  const hipError_t e = bf16          ? (A.N <= 32   ? launch_walks<1, 1>(A, U, stream)
+                                        : A.N <= 64 ? launch_walks<1, 2>(A, U, stream)
+                                                    : launch_walks<1, 4>(A, U, stream))
+                       : A.N <= 32 ? launch_walks<3, 1>(A, U, stream)
+                       : A.N <= 64 ? launch_walks<3, 2>(A, U, stream)
+                                   : launch_walks<3, 4>(A, U, stream);
+  if (e != hipSuccess || A.segments == 1) return e;
+  hipLaunchKernelGGL(scan_joins_kernel, dim3(2 * join_groups(A)), dim3(256), 0, stream, A, U);
+  return hipGetLastError();
 }
 
 }  // namespace sdm

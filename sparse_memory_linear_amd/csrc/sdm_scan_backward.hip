@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
   constexpr int Q = TL::Q, NP = TL::NP, QT = TL::QT, NT = TL::NT, MT = TL::MT;
   constexpr int LB = TL::LB, LX = TL::LX, LM = TL::LM, LU = TL::LU, nB = TL::nB, nX = TL::nX, nM = TL::nM, nU = TL::nU;
   extern __shared__ __align__(16) uint16_t lds[];
-  __shared__ __align__(16) double l_[Q], row_[MT][16], col_[MT][16], us_[kWaves];
-  __shared__ __align__(16) float step_[Q], since_[Q], left_[Q], w_[Q], up_[Q], diag_[Q], trace_[Q];
+  __shared__ __align__(16) double l_[Q], row_[2][MT][16], col_[2][MT][16], us_[kWaves];
+  __shared__ __align__(16) float step_[Q], since_[Q], left_[Q], w_[Q], up_[Q], diag_[2][Q], trace_[2][Q];
   __shared__ __align__(16) float read_[NT][Q], put_[NT][Q];
   uint16_t *Bs = lds, *Cs = Bs + NP * nB, *Xs = Cs + NP * nB, *Gs = Xs + NP * nX, *Ms = Gs + 3 * nX, *Rs = Ms + 3 * nM,
            *Us = Ms;
@@ -206,6 +206,56 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
   // down again for the rest, then the next head's first
   const int plast = (pblocks - 1) * kPB;
   fetch(h0, 0);
+  double l_ahead;
+  float step_ahead, dt_ahead;
+  auto fetch_gates = [&](int h) {
+    const long long gate = ((long long)b * A.H + h) * R.stride + t0 + (lane & (Q - 1));
+    l_ahead = R.l[gate];
+    step_ahead = R.step[gate];
+    dt_ahead = A.dt[(row0 + min(lane, here - 1)) * A.ld_dt + h];
+  };
+  fetch_gates(h0);
+
+  // ---- time steps of a head, one token per lane of a wave; the last wave does it beside the next head's M
+  // and R, of which it has the fewest tiles
+  int side = 0;  // where this head's sums go
+  auto times = [&](int h, float step, float raw, double end) {
+    anew();
+    const int i = lane & (Q - 1), own = i / 16;
+    double row = 0.0, col = 0.0, rd = 0.0, pu = 0.0, whole = 0.0;
+#pragma unroll
+    for (int u = 0; u < QT; ++u) {  // tiles of the token's row, and of its column
+      const int lo = min(own, u), hi = max(own, u), t = lo == hi ? own : QT + hi * (hi - 1) / 2 + lo;
+      const double a = row_[side ^ 1][t][i & 15], c = col_[side ^ 1][t][i & 15];
+      row += u <= own ? a : 0.0;
+      col += u >= own ? c : 0.0;
+    }
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      rd += (double)read_[k][i];
+      pu += (double)put_[k][i];
+    }
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) whole += us_[k];
+    const bool in = lane < here;
+    const float rate = -expf(A.A_log[h]);
+    const double st = (double)step;
+    const double ahead = in ? row - st * col + rd : 0.0, behind = in ? st * pu : 0.0;
+    const double pa = block_prefix<64>(ahead), pp = block_prefix<64>(behind);
+    const double dl = read_lane(pa, 63) - pa + ahead + pp - behind + (double)exp2_of(end) * whole;
+    double ddt = 0.0, da = 0.0, tr = 0.0;
+    if (in) {
+      ddt = ((double)diag_[side ^ 1][i] + col + pu + dl * (double)rate) * (double)(1.f / (1.f + expf(-raw)));
+      da = dl * (double)rate * st;
+      tr = (double)trace_[side ^ 1][i];
+    }
+    if (lane < rows) A.ddt[(row0 + lane) * A.ld_dt + h] = (float)ddt;
+    const double s0 = read_lane(block_prefix<64>(da), 63), s1 = read_lane(block_prefix<64>(ddt), 63),
+                 s2 = read_lane(block_prefix<64>(tr), 63);
+    if (lane < 3) W.sums[(((long long)b * W.blocks + blk) * A.H + h) * 3 + lane] = lane == 0 ? s0 : lane == 1 ? s1 : s2;
+  };
+  float step_before = 0.f, raw_before = 0.f;
+  double end_before = 0.0;
   for (int h = h0; h < h1; ++h) {
     anew();
     const long long bh = (long long)b * A.H + h;
@@ -219,10 +269,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
     const rsrc_t rows_uf = block_rows(W.U_first + ((long long)useg * A.B * A.H + bh) * P * N, split ? state : 0u);
     const float upto_s = split ? W.S_upto[bh * W.blocks + blk] : 0.f, upto_u = split ? W.U_upto[bh * W.blocks + blk] : 0.f;
     // ---- gates, by every wave in its lanes, one of them each into LDS
-    const long long gate = bh * R.stride + t0 + (lane & (Q - 1));
-    const double l = R.l[gate];
-    const float step = R.step[gate];
-    const float raw = lane < here ? A.dt[(row0 + lane) * A.ld_dt + h] + A.dt_bias[h] : 0.f;
+    const double l = l_ahead;
+    const float step = step_ahead, raw = dt_ahead + A.dt_bias[h];
     const double end = read_lane(l, Q - 1);
     if (lane < Q) {
       if (wave == 0) l_[lane] = l;
@@ -262,6 +310,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
         }
     }
 
+    fetch_gates(min(h + 1, h1 - 1));
+    if (wave == kWaves - 1 && h > h0) times(h - 1, step_before, raw_before, end_before);
     anew();
     // ---- M and R (R's columns in the order of across()), sums over rows and columns of F
 #pragma unroll
@@ -299,8 +349,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
           m[u] = ge * st[u] + __uint_as_float(__float_as_uint(D) & self);
           r[u] = pe * st[u];
           if (self) {
-            diag_[i] = f;
-            trace_[i] = Pm[e][u];
+            diag_[side][i] = f;
+            trace_[side][i] = Pm[e][u];
           }
           const double off = (double)__uint_as_float(__float_as_uint(f) & ~self);
           col[u] = off;
@@ -309,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
         // over the columns: the four groups of 16 lanes; over the rows: the lanes of a group
         row += __shfl_xor(row, 16, 64);
         row += __shfl_xor(row, 32, 64);
-        if (lg == 0) row_[t][lr] = row;
+        if (lg == 0) row_[side][t][lr] = row;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           double v = col[u];
@@ -317,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
           v = add_dpp<0x112, 0xF>(v);
           v = add_dpp<0x114, 0xF>(v);
           v = add_dpp<0x118, 0xF>(v);
-          if (lr == 15) col_[t][4 * lg + u] = v;
+          if (lr == 15) col_[side][t][4 * lg + u] = v;
         }
       }
       uint32_t a[3], d[3];
@@ -484,43 +534,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
     if (lane == 63) us_[wave] = us;
     __syncthreads();
 
-    // ---- time steps: one token per lane of wave 0
-    if (wave == 0) {
-      anew();
-      const int i = lane & (Q - 1), own = i / 16;
-      double row = 0.0, col = 0.0, rd = 0.0, pu = 0.0, whole = 0.0;
-#pragma unroll
-      for (int u = 0; u < QT; ++u) {  // tiles of the token's row, and of its column
-        const int lo = min(own, u), hi = max(own, u), t = lo == hi ? own : QT + hi * (hi - 1) / 2 + lo;
-        const double a = row_[t][i & 15], c = col_[t][i & 15];
-        row += u <= own ? a : 0.0;
-        col += u >= own ? c : 0.0;
-      }
-#pragma unroll
-      for (int k = 0; k < NT; ++k) {
-        rd += (double)read_[k][i];
-        pu += (double)put_[k][i];
-      }
-#pragma unroll
-      for (int k = 0; k < kWaves; ++k) whole += us_[k];
-      const bool in = lane < here;
-      const float rate = -expf(A.A_log[h]);
-      const double st = (double)step;
-      const double ahead = in ? row - st * col + rd : 0.0, behind = in ? st * pu : 0.0;
-      const double pa = block_prefix<64>(ahead), pp = block_prefix<64>(behind);
-      const double dl = read_lane(pa, 63) - pa + ahead + pp - behind + (double)exp2_of(end) * whole;
-      double ddt = 0.0, da = 0.0, tr = 0.0;
-      if (in) {
-        ddt = ((double)diag_[i] + col + pu + dl * (double)rate) * (double)(1.f / (1.f + expf(-raw)));
-        da = dl * (double)rate * st;
-        tr = (double)trace_[i];
-      }
-      if (lane < rows) A.ddt[(row0 + lane) * A.ld_dt + h] = (float)ddt;
-      const double s0 = read_lane(block_prefix<64>(da), 63), s1 = read_lane(block_prefix<64>(ddt), 63),
-                   s2 = read_lane(block_prefix<64>(tr), 63);
-      if (lane < 3) W.sums[(((long long)b * W.blocks + blk) * A.H + h) * 3 + lane] = lane == 0 ? s0 : lane == 1 ? s1 : s2;
-    }
+    step_before = step;
+    raw_before = raw;
+    end_before = end;
+    side ^= 1;
   }
+  if (wave == kWaves - 1) times(h1 - 1, step_before, raw_before, end_before);
 
   if (owns) {
     const int k = 16 * nt + 4 * lg;

@@ -290,6 +290,18 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
     }
     if (wave == 7 && lane < Q) up_[lane] = exp2_of(l - from);
 
+    // U of a channel block, fetched while the products before it run
+    uint4 ru[UN], uf_[UN];
+    auto fetch_u = [&](int p0) {
+#pragma unroll
+      for (int i = 0; i < UN; ++i) {
+        const int v = tid + kThreads * i, p = v / UR, k = v % UR * 4;
+        const uint32_t at = p0 + p < P && k < N ? (uint32_t)((p0 + p) * N + k) * 4 : kNowhere;
+        ru[i] = load16(rows_u, at);
+        uf_[i] = load16(rows_uf, at);
+      }
+    };
+
     // ---- P = go x^T over the channel blocks; the last one's tiles stay
     f32x4_t Pm[MW];
 #pragma unroll
@@ -397,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
         }
       }
     }
+    fetch_u(plast);
     f32x4_t T1[TW], T2[TW];
 #pragma unroll
     for (int r = 0; r < TW; ++r) T1[r] = T2[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -438,15 +451,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
         }
         __syncthreads();
       }
-      // U of the channel block, and S^T for the states' share: d_k of this lane, 8 channels a step
-      uint4 ru[UN], uf_[UN], rs[kPB / 32][2], sf_[kPB / 32][2];
-#pragma unroll
-      for (int i = 0; i < UN; ++i) {
-        const int v = tid + kThreads * i, p = v / UR, k = v % UR * 4;
-        const uint32_t at = p0 + p < P && k < N ? (uint32_t)((p0 + p) * N + k) * 4 : kNowhere;
-        ru[i] = load16(rows_u, at);
-        uf_[i] = load16(rows_uf, at);
-      }
+      // S^T for the state's share: d_k of this lane, 8 channels a step
+      uint4 rs[kPB / 32][2], sf_[kPB / 32][2];
 #pragma unroll
       for (int k = 0; k < kPB / 32; ++k) {
         const int p = p0 + 32 * k + 8 * lg, kk = 16 * nt + lr;
@@ -498,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
           }
         }
       }
+      if (pb > 0) fetch_u(p0 - kPB);
       const int pp = p0 + 32 * (pt >> 1) + 8 * lg + 4 * (pt & 1);
 #pragma unroll
       for (int r = 0; r < JW; ++r) {

@@ -237,6 +237,18 @@ inline size_t gates_bytes(long long units, int T, char* base, ScanGates* g) {
 }
 hipError_t launch_scan_gates(const ScanArgs& A, int Q, const ScanGates& g, hipStream_t stream);
 
+// Turned states, as the gradient's blocks take S: the operand pieces of its products in their lanes' order,
+// [d_k / 16][d_v / 32][2 halves][64 lanes][4 channels], where lane 16 g + r has d_k r and channels 8 g .. 8 g + 7,
+// with d_k up to 32, 64 or 128 and d_v up to a multiple of 64. A wave loads 1 KB in a row with each instruction;
+// as [d_k][d_v] its lanes' pieces lay 512 bytes apart.
+__host__ __device__ inline int turned_dk(int N) { return N <= 32 ? 32 : N <= 64 ? 64 : 128; }
+__host__ __device__ inline int turned_dv(int P) { return (P + 63) / 64 * 64; }
+__host__ __device__ inline int turned_size(int N, int P) { return turned_dk(N) * turned_dv(P); }
+// (in floats; p in whole halves)
+__device__ __forceinline__ int turned_at(int tile, int P, int p, int r) {
+  return (((tile * (turned_dv(P) / 32) + p / 32) * 2 + p / 4 % 2) * 64 + p / 8 % 4 * 16 + r) * 4;
+}
+
 // One walk over the blocks (sdm_scan_states.hip): token t of (b, h) has X at b xb + h xh + t ld_x, K at
 // (b T + t) ld_k + g N, its weight and log-decay at (b H + h) stride + t.
 struct ScanWalk {
@@ -248,11 +260,11 @@ struct ScanWalk {
   const double* l;
   const float* start;  // state before the walk, or null
   float* end;          // state behind it, or null
-  // of several segments: [segments + 1][B*H][P][N] states before them (forward with `states`: [N][P]), the last
+  // of several segments: [segments + 1][B*H][P][N] states before them (forward with `states`: turned), the last
   // place for what the last one adds; and [segments + 1][B*H] log2 of the decay of the segment before
   float* first;
   double* decay;
-  // [B*H][blocks] what the segment adds to the states entering the blocks, forward [N][P], backward [P][N], and
+  // [B*H][blocks] what the segment adds to the states entering the blocks, forward turned, backward [P][N], and
   // [B*H][blocks] the decay from the segment's start to there; null: only `first` is wanted
   float *states, *upto;
 };

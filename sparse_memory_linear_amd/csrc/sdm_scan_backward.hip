@@ -33,7 +33,7 @@ constexpr int kWaves = 8, kThreads = 64 * kWaves;
 
 struct ScanBwd {
   // The states before the blocks and the gradients behind them, in segments of blocks: what the segment adds,
-  // [B*H][blocks] of [N][P] and of [P][N], and, of several segments, the states before those,
+  // [B*H][blocks] of turned states and of [P][N], and, of several segments, the states before those,
   // [segments][B*H], and the factors they take for the block, [B*H][blocks]
   const float *S, *U, *S_first, *U_first, *S_upto, *U_upto;
   int segments;
@@ -263,9 +263,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
     // S and U: what the segment adds (nothing before its first block), and of several segments what was before it
     const uint32_t state = (uint32_t)(P * N) * 4;
     const bool split = W.segments > 1;
-    const rsrc_t rows_s = block_rows(W.S + (bh * W.blocks + blk) * P * N, split && blk == seg_s ? 0u : state);
+    const int turned = turned_size(N, P);
+    const rsrc_t rows_s = block_rows(W.S + (bh * W.blocks + blk) * turned, split && blk == seg_s ? 0u : (uint32_t)turned * 4);
     const rsrc_t rows_u = block_rows(W.U + (bh * W.blocks + blk) * P * N, split && blk == seg_u ? 0u : state);
-    const rsrc_t rows_sf = block_rows(W.S_first + ((long long)sseg * A.B * A.H + bh) * P * N, split ? state : 0u);
+    const rsrc_t rows_sf = block_rows(W.S_first + ((long long)sseg * A.B * A.H + bh) * turned, split ? (uint32_t)turned * 4 : 0u);
     const rsrc_t rows_uf = block_rows(W.U_first + ((long long)useg * A.B * A.H + bh) * P * N, split ? state : 0u);
     const float upto_s = split ? W.S_upto[bh * W.blocks + blk] : 0.f, upto_u = split ? W.U_upto[bh * W.blocks + blk] : 0.f;
     // ---- gates, by every wave in its lanes, one of them each into LDS
@@ -456,11 +457,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
 #pragma unroll
       for (int k = 0; k < kPB / 32; ++k) {
         const int p = p0 + 32 * k + 8 * lg, kk = 16 * nt + lr;
-        const uint32_t at = p < P && kk < N ? (uint32_t)(kk * P + p) * 4 : kNowhere;
+        const uint32_t at = p < P && kk < N ? (uint32_t)turned_at(nt, P, p, lr) * 4 : kNowhere;
         rs[k][0] = load16(rows_s, at);
-        rs[k][1] = load16(rows_s, at + 16);
+        rs[k][1] = load16(rows_s, at + 1024);
         sf_[k][0] = load16(rows_sf, at);
-        sf_[k][1] = load16(rows_sf, at + 16);
+        sf_[k][1] = load16(rows_sf, at + 1024);
       }
 #pragma unroll
       for (int r = 0; r < JW; ++r)
@@ -607,7 +608,7 @@ struct BwdPlan {
 BwdPlan plan_of(const sdm_scan_shape& S, char* base) {
   BwdPlan L{};
   const int Q = S.in_dtype == SDM_BF16 ? 64 : 32, hpg = S.H / S.G;
-  const size_t units = (size_t)S.B * S.H, state = (size_t)S.d_v * S.d_k * 4;
+  const size_t units = (size_t)S.B * S.H, state = (size_t)S.d_v * S.d_k * 4, turned = (size_t)turned_size(S.d_k, S.d_v) * 4;
   L.bwd.blocks = (S.T + Q - 1) / Q;
   const long long groups = (long long)S.B * S.G * L.bwd.blocks;
   long long parts = 1;
@@ -626,7 +627,7 @@ BwdPlan plan_of(const sdm_scan_shape& S, char* base) {
   L.bwd.segments = scan_segments((long long)units * ((S.d_v + kPB - 1) / kPB), L.bwd.blocks, 256);
   size_t at = gates_bytes(units, S.T, base, &L.gates);
   L.bwd.S = (float*)(base + at);
-  at += align_up(units * L.bwd.blocks * state);
+  at += align_up(units * L.bwd.blocks * turned);
   L.bwd.U = (float*)(base + at);
   at += align_up(units * L.bwd.blocks * state);
   L.bwd.sums = (double*)(base + at);
@@ -638,8 +639,9 @@ BwdPlan plan_of(const sdm_scan_shape& S, char* base) {
   if (L.bwd.segments > 1) {
     const size_t slots = units * (L.bwd.segments + 1), factors = align_up(units * L.bwd.blocks * 4);
     L.bwd.S_first = (float*)(base + at);
-    L.bwd.U_first = (float*)(base + at + align_up(slots * state));
-    at += 2 * align_up(slots * state);
+    at += align_up(slots * turned);
+    L.bwd.U_first = (float*)(base + at);
+    at += align_up(slots * state);
     L.decay = (double*)(base + at);
     L.decay_back = (double*)(base + at + align_up(slots * 8));
     at += 2 * align_up(slots * 8);

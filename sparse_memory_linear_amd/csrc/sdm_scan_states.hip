@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(256) scan_gates_kernel(ScanArgs A, ScanGates g
 // state before the segment, which is known only behind this walk, still has to be multiplied. So one pass over
 // the tokens does: a pass for the segments' ends first took 33 us more (4 x 2048 tokens, 8 heads of 128 x 128).
 // A walk of one segment starts from the call's state and stores all.
-// TURN: results as [channel][d_k] tiles, whose lanes hold 4 consecutive channels, and states as [d_k][d_v]; else
+// TURN: results as [channel][d_k] tiles, whose lanes hold 4 consecutive channels, and turned states; else
 // the other way round. Each is stored the way the products that read it take it.
 constexpr int kPB = 64;
 
@@ -110,22 +110,25 @@ __device__ __forceinline__ void walk(const ScanWalk& A, int id, uint16_t* lds, f
 
   // where the four values of tile m lie in a state of the walk's own layout (-1: nowhere)
   auto place = [&](int m) {
-    const int p = p0 + 16 * wave + (TURN ? 4 * lg : lr), k = 16 * m + (TURN ? lr : 4 * lg);
-    return p < P && k < N ? (TURN ? k * P + p : p * N + k) : -1;
+    if (TURN) return turned_at(m, P, p0 + 16 * wave + 4 * lg, lr);
+    const int p = p0 + 16 * wave + lr, k = 16 * m + 4 * lg;
+    return p < P && k < N ? p * N + k : -1;
   };
+  const int size = TURN ? turned_size(N, P) : P * N;
   f32x4_t S[NT];
   const float* start = A.segments == 1 && A.start ? A.start + bh * P * N : nullptr;
 #pragma unroll
   for (int m = 0; m < NT; ++m) {
     const int at = place(m);
     S[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    if (start && at >= 0) {
-      if (TURN) {  // [d_v][d_k]
+    if (TURN && start) {  // [d_v][d_k]
+      const int p = p0 + 16 * wave + 4 * lg, k = 16 * m + lr;
+      if (p < P && k < N) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[m][e] = start[(at % P + e) * N + at / P];
-      } else {
-        S[m] = *(const f32x4_t*)(start + at);
+        for (int e = 0; e < 4; ++e) S[m][e] = start[(p + e) * N + k];
       }
+    } else if (start && at >= 0) {
+      S[m] = *(const f32x4_t*)(start + at);
     }
   }
   double total = 0.0;
@@ -133,9 +136,9 @@ __device__ __forceinline__ void walk(const ScanWalk& A, int id, uint16_t* lds, f
   auto block = [&](int step, int set) {
     const int c = BACK ? A.blocks - 1 - step : step;
     if (BLOCKS) {
-      float* to = A.states + (bh * A.blocks + c) * P * N;
+      float* to = A.states + (bh * A.blocks + c) * size;
       // (nothing of a segment's first block, but the same stores)
-      const rsrc_t all = block_rows(to, A.segments == 1 || step > s0 ? (uint32_t)(P * N) * 4 : 0u);
+      const rsrc_t all = block_rows(to, A.segments == 1 || step > s0 ? (uint32_t)size * 4 : 0u);
       if (A.upto && tid == 0 && pb == 0) A.upto[bh * A.blocks + c] = exp2_of(total);
 #pragma unroll
       for (int m = 0; m < NT; ++m) {
@@ -185,7 +188,7 @@ __device__ __forceinline__ void walk(const ScanWalk& A, int id, uint16_t* lds, f
     block(step, 0);
     if (step + 1 < s1) block(step + 1, 1);
   }
-  float* to = A.segments > 1 ? A.first + ((long long)(seg + 1) * A.B * A.H + bh) * P * N
+  float* to = A.segments > 1 ? A.first + ((long long)(seg + 1) * A.B * A.H + bh) * size
               : A.end        ? A.end + bh * P * N
                              : nullptr;
   if (to) {  // (a turned walk of one segment has no end)
@@ -218,18 +221,19 @@ __global__ void __launch_bounds__(256, 2) scan_walks_kernel(ScanWalk A, ScanWalk
 
 // States before the segments, from the segments' own ends: first[0] is the call's first state, first[s]
 // (which holds what segment s-1 adds) takes up first[s-1] decayed over segment s-1, and so the call's end.
-// `turned`: of [d_k][d_v].
 __device__ __forceinline__ void join(const ScanWalk& A, bool turned, long long group) {
-  const long long per = (long long)A.P * A.N / 4, units = (long long)A.B * A.H;
+  const long long per = (turned ? turned_size(A.N, A.P) : A.P * A.N) / 4, units = (long long)A.B * A.H;
   const long long i = group * 256 + threadIdx.x;
   if (i >= units * per) return;
   f32x4_t* v = (f32x4_t*)A.first;
   f32x4_t s = {0.f, 0.f, 0.f, 0.f};
   if (A.start && turned) {
-    const long long unit = i / per;
-    const int at = (int)(i % per) * 4;
+    const int at = (int)(i % per), lane = at % 64, tiles = turned_dv(A.P) / 32;
+    const int p = at / 128 % tiles * 32 + lane / 16 * 8 + at / 64 % 2 * 4, k = at / 128 / tiles * 16 + lane % 16;
+    if (p < A.P && k < A.N) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] = A.start[unit * per * 4 + (at % A.P + e) * A.N + at / A.P];
+      for (int e = 0; e < 4; ++e) s[e] = A.start[(i / per * A.P + p + e) * A.N + k];
+    }
   } else if (A.start) {
     s = ((const f32x4_t*)A.start)[i];
   }
@@ -255,13 +259,15 @@ __device__ __forceinline__ void join(const ScanWalk& A, bool turned, long long g
 }
 
 __global__ void __launch_bounds__(256) scan_join_kernel(ScanWalk A) { join(A, false, blockIdx.x); }
-__global__ void __launch_bounds__(256) scan_joins_kernel(ScanWalk A, ScanWalk U) {
-  const int half = gridDim.x / 2;
-  if ((int)blockIdx.x < half) join(A, true, blockIdx.x);
-  else join(U, false, blockIdx.x - half);
+__global__ void __launch_bounds__(256) scan_joins_kernel(ScanWalk A, ScanWalk U, int first) {
+  if ((int)blockIdx.x < first) join(A, true, blockIdx.x);
+  else join(U, false, blockIdx.x - first);
 }
 
-unsigned join_groups(const ScanWalk& A) { return (unsigned)(((long long)A.B * A.H * A.P * A.N / 4 + 255) / 256); }
+unsigned join_groups(const ScanWalk& A, bool turned) {
+  const int size = turned ? turned_size(A.N, A.P) : A.P * A.N;
+  return (unsigned)(((long long)A.B * A.H * (size / 4) + 255) / 256);
+}
 unsigned walk_groups(const ScanWalk& A) { return (unsigned)((long long)A.B * A.H * ((A.P + kPB - 1) / kPB) * A.segs); }
 constexpr int walk_lds(int XP, int KP, int NK) {
   return (KP * (KP == 1 ? 64 : 32) * (NK * 32 + 16) + XP * (KP == 1 ? 64 : 32) * (kPB + 16)) * 2;
@@ -300,7 +306,7 @@ hipError_t launch_scan_walk(const ScanWalk& A, bool bf16, hipStream_t stream) {
                  : A.N <= 64 ? launch_walk<3, 2>(A, stream)
                              : launch_walk<3, 4>(A, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(scan_join_kernel, dim3(join_groups(A)), dim3(256), 0, stream, A);
+  hipLaunchKernelGGL(scan_join_kernel, dim3(join_groups(A, false)), dim3(256), 0, stream, A);
   return hipGetLastError();
 }
 
@@ -312,7 +318,8 @@ hipError_t launch_scan_walks(const ScanWalk& A, const ScanWalk& U, bool bf16, hi
                        : A.N <= 64 ? launch_walks<3, 2>(A, U, stream)
                                    : launch_walks<3, 4>(A, U, stream);
   if (e != hipSuccess || A.segments == 1) return e;
-  hipLaunchKernelGGL(scan_joins_kernel, dim3(2 * join_groups(A)), dim3(256), 0, stream, A, U);
+  const unsigned first = join_groups(A, true);
+  hipLaunchKernelGGL(scan_joins_kernel, dim3(first + join_groups(U, false)), dim3(256), 0, stream, A, U, (int)first);
   return hipGetLastError();
 }
 

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
   constexpr int E = BF16 ? 8 : 4, ES = BF16 ? 2 : 4;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 
-  // ---- B, C of the block and G = C B^T, tile t = wave + 8 e as [j][i]
+  // ---- B, C of the block and G = C B^T, tile t = wave + 7 e as [j][i]
   {
     constexpr int KR = NK * 32 / E, KN = (Q * KR + kThreads - 1) / kThreads;
 #pragma unroll
@@ -134,12 +134,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
     }
   }
   __syncthreads();
-  constexpr int MW = (MT + QT / 2 + kWaves - 1) / kWaves;  // tiles per wave, the zero tiles behind the others
+  // tiles per wave, the zero tiles behind the others; the last wave, which does the time steps, has none
+  constexpr int MW = (MT + QT / 2 + kWaves - 2) / (kWaves - 1);
+  const int tile0 = wave < kWaves - 1 ? wave : MT + QT / 2;
   int it_[MW], jt_[MW];
   f32x4_t G[MW];
 #pragma unroll
   for (int e = 0; e < MW; ++e) {
-    const int t = wave + kWaves * e;
+    const int t = tile0 + (kWaves - 1) * e;
     int it = 1, jt = t - QT;
     while (jt >= it) jt -= it++;
     it_[e] = t < QT ? t : t < MT ? it : 2 * (t - MT);
@@ -216,8 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
   };
   fetch_gates(h0);
 
-  // ---- time steps of a head, one token per lane of a wave; the last wave does it beside the next head's M
-  // and R, of which it has the fewest tiles
+  // ---- time steps of a head, one token per lane of a wave: the last one, beside the others' M and R of the next head
   int side = 0;  // where this head's sums go
   auto times = [&](int h, float step, float raw, double end) {
     anew();
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
       __syncthreads();
 #pragma unroll
       for (int e = 0; e < MW; ++e)
-        if (wave + kWaves * e < MT) {
+        if (tile0 + (kWaves - 1) * e < MT) {
 #pragma unroll
           for (int k = 0; k < kPB / 32; ++k)
             mma(Pm[e], along<NP>(Xs + 16 * jt_[e] * LX + 32 * k, LX, nX, lane), along<3>(Gs + 16 * it_[e] * LX + 32 * k, LX, nX, lane));
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
     // ---- M and R (R's columns in the order of across()), sums over rows and columns of F
 #pragma unroll
     for (int e = 0; e < MW; ++e) {
-      const int t = wave + kWaves * e;
+      const int t = tile0 + (kWaves - 1) * e;
       if (t >= MT + QT / 2) break;
       const int i = 16 * it_[e] + lr, j = 16 * jt_[e] + 4 * lg;
       float m[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs A, 
         else if (h + 1 < h1) fetch(h + 1, 0);
 #pragma unroll
         for (int e = 0; e < MW; ++e) {
-          const int t = wave + kWaves * e;
+          const int t = tile0 + (kWaves - 1) * e;
           if (t >= MT + QT / 2) break;
           const int i = 16 * it_[e] + lr, j = 16 * jt_[e] + 4 * lg;
           float m[4] = {0.f, 0.f, 0.f, 0.f};

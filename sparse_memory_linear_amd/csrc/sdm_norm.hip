@@ -189,30 +189,85 @@ __global__ void __launch_bounds__(WPR > 4 ? 64 * WPR : 256, WPR > 8 ? 4 : NC * W
     }
   };
 
+  // A row's values as they lie in memory: with one octet a lane the next row's are under way while a row is
+  // worked on, and the weights stay
+  constexpr bool AHEAD = NC == 1;
+  struct Octet {
+    uint4 a, b;  // (bf16: a)
+  } ry[NC], rr[NC], rt[NC], rd[NC];
+  auto fetch = [&](long long row) {  // (-1: none)
+    const int hi = __builtin_amdgcn_readfirstlane((int)(row >> 32)), lo = __builtin_amdgcn_readfirstlane((int)row);
+    const long long m = (long long)hi << 32 | (uint32_t)lo;  // (a wave's own)
+    auto row_of = [&](const void* base, bool bf16, bool there) {
+      return block_rows((const char*)base + m * A.D * (bf16 ? 2 : 4), there && m >= 0 ? (uint32_t)A.D * (bf16 ? 2 : 4) : 0u);
+    };
+    auto octet = [&](rsrc_t r, bool bf16, int o) {
+      const uint32_t at = o < octets ? (uint32_t)o * (bf16 ? 16 : 32) : kNowhere;
+      return Octet{load16(r, at), load16(r, bf16 ? kNowhere : at + 16)};
+    };
+    const rsrc_t y = row_of(A.y, A.y_bf16, true), r = row_of(A.r, A.r_bf16, true), x = row_of(A.dx, false, A.w_pre != nullptr),
+                 d = row_of(A.dr_out, false, A.dr_out != nullptr);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      ry[i] = octet(y, A.y_bf16, lane + i * LANES);
+      rr[i] = octet(r, A.r_bf16, lane + i * LANES);
+      rt[i] = octet(x, false, lane + i * LANES);
+      rd[i] = octet(d, false, lane + i * LANES);
+    }
+  };
+  auto values = [](const Octet& q, bool bf16, float (&v)[8]) {
+    const float f[8] = {__uint_as_float(q.a.x), __uint_as_float(q.a.y), __uint_as_float(q.a.z), __uint_as_float(q.a.w),
+                        __uint_as_float(q.b.x), __uint_as_float(q.b.y), __uint_as_float(q.b.z), __uint_as_float(q.b.w)};
+    const float h[8] = {bf16lo(q.a.x), bf16hi(q.a.x), bf16lo(q.a.y), bf16hi(q.a.y),
+                        bf16lo(q.a.z), bf16hi(q.a.z), bf16lo(q.a.w), bf16hi(q.a.w)};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = bf16 ? h[e] : f[e];
+  };
+  float kept_post[8] = {}, kept_pre[8] = {};
+  if (AHEAD && lane < octets) {
+    if (A.w_post) load8<false>(A.w_post, lane * 8, kept_post);
+    if (A.w_pre) load8<false>(A.w_pre, lane * 8, kept_pre);
+  }
+  auto weight = [&](const float* all, const float (&kept)[8], int o, float (&v)[8]) {
+    if (!AHEAD) {
+      if (all) load8<false>(all, o * 8, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = kept[e];
+    }
+  };
+
   float sg[NC][8] = {}, sp[NC][8] = {}, sn[NC][8] = {};
   const bool summed = A.gate && per_gate > 1;  // a gate of each token has no sums
+  auto group_end = [&](long long g0) {
+    const long long end = summed ? (g0 / per_gate + 1) * per_gate : m1;
+    return end < m1 ? end : m1;
+  };
+  auto row_at = [&](long long mm, long long g1) { return mm + slot < g1 ? mm + slot : g1 - 1; };
+  if (AHEAD && m0 < m1) fetch(row_at(m0, group_end(m0)));
   for (long long g0 = m0; g0 < m1;) {
-    const long long grp = g0 / per_gate, end = summed ? (grp + 1) * per_gate : m1, g1 = end < m1 ? end : m1;
+    const long long grp = g0 / per_gate, end = summed ? (grp + 1) * per_gate : m1, g1 = group_end(g0);
     for (long long mm = g0; mm < g1; mm += SLOTS) {
       const bool live = mm + slot < g1;
-      const long long m = live ? mm + slot : g1 - 1;
-      if (!live && WPR == 1) break;  // (with more waves a row all of them meet at the sums)
+      const long long m = row_at(mm, g1);  // (behind the last: that again, for nothing)
       const long long gate_row = m / per_gate * A.D;
       turn ^= 1;
       float yn[NC][8], h[NC][8], t[NC][8], dr[NC][8];
       float ss = 0.f, none = 0.f;
+      if (!AHEAD) fetch(m);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int o = lane + i * LANES;
         if (o < octets) {
-          load8_rt(A.y, A.y_bf16, m * A.D + o * 8, yn[i]);
-          load8_rt(A.r, A.r_bf16, m * A.D + o * 8, h[i]);
-          if (A.w_pre) load8<false>(A.dx, m * A.D + o * 8, t[i]);
-          if (A.dr_out) load8<false>(A.dr_out, m * A.D + o * 8, dr[i]);
+          values(ry[i], A.y_bf16, yn[i]);
+          values(rr[i], A.r_bf16, h[i]);
+          values(rt[i], false, t[i]);
+          values(rd[i], false, dr[i]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) ss = fmaf(yn[i][e], yn[i][e], ss);
         }
       }
+      if (AHEAD) fetch(mm + SLOTS < g1 ? row_at(mm + SLOTS, g1) : g1 < m1 ? row_at(g1, group_end(g1)) : -1);
       float p = 1.f;
       if (A.w_post) {
         row_sum(ss, none, 0);
@@ -224,9 +279,9 @@ __global__ void __launch_bounds__(WPR > 4 ? 64 * WPR : 256, WPR > 8 ? 4 : NC * W
         const int o = lane + i * LANES;
         if (o < octets) {
           float w[8], g[8], wn[8];
-          if (A.w_post) load8<false>(A.w_post, o * 8, w);
+          weight(A.w_post, kept_post, o, w);
+          weight(A.w_pre, kept_pre, o, wn);
           if (A.gate) load8_rt(A.gate, A.g_bf16, gate_row + o * 8, g);
-          if (A.w_pre) load8<false>(A.w_pre, o * 8, wn);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             yn[i][e] *= p;
@@ -250,12 +305,12 @@ __global__ void __launch_bounds__(WPR > 4 ? 64 * WPR : 256, WPR > 8 ? 4 : NC * W
         const int o = lane + i * LANES;
         if (o < octets) {
           float w[8], g[8], wn[8], dg[8];
-          if (A.w_post) load8<false>(A.w_post, o * 8, w);
+          weight(A.w_post, kept_post, o, w);
+          weight(A.w_pre, kept_pre, o, wn);
           if (A.gate) load8_rt(A.gate, A.g_bf16, gate_row + o * 8, g);
-          if (A.w_pre) load8<false>(A.w_pre, o * 8, wn);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            float d = A.dr_out ? dr[i][e] : 0.f;
+            float d = dr[i][e];
             if (A.w_pre) {
               const float hn = h[i][e] * q;
               d += q * (t[i][e] * wn[e] - hn * mean);

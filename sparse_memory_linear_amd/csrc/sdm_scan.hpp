@@ -19,7 +19,6 @@ constexpr float kMaxDecay = 1000.f;  // floor of a token's log-decay (exp(-1000)
 constexpr double kLog2e = 1.4426950408889634074;
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
@@ -31,25 +30,6 @@ __device__ __forceinline__ float scan_val(const void* p, long long at) {
 __device__ __forceinline__ float softplus(float x) { return x > 20.f ? x : log1pf(expf(x)); }
 
 __device__ __forceinline__ float exp2_of(double x) { return __builtin_amdgcn_exp2f((float)x); }
-
-// The rows of a block as a buffer: 16 bytes from an offset, zeros from `bytes` on, where stores are dropped.
-// Rows behind a sequence's end and columns that are not there (kNowhere) so need no branch and no 64-bit
-// address of their own; and a wave waits for its older loads alone, where a branch around newer accesses would
-// have it wait for those too.
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-constexpr uint32_t kNowhere = 0x80000000u;
-__device__ __forceinline__ rsrc_t block_rows(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
-}
-__device__ __forceinline__ uint4 load16(rsrc_t rows, uint32_t at) {
-  const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(rows, (int)at, 0, 0);
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
-__device__ __forceinline__ void store16(rsrc_t rows, uint32_t at, f32x4_t v) {
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rows, (int)at, 0, 0);
-}
 
 // High halves of two words as one word (a in the low half)
 __device__ __forceinline__ uint32_t high_halves(float a, float b) {

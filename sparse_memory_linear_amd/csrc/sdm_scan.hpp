@@ -249,13 +249,15 @@ struct ScanWalk {
   float *states, *upto;
 };
 // Segments of a walk (or of the forward kernel): a call of few units is split until `wanted` workgroups are
-// busy, each with at least four blocks, so that enough share the pass that finds the segments' first states.
+// busy, but for s segments of n blocks the walk and the kernel behind it take about 4 us per block, n / s in a
+// row, and the join 1 us per 8 segments, so s stays below sqrt(32 n): 25 us for 1024 tokens of 8 heads (36 with
+// at least four blocks each), 99 us for 131072 tokens of one head (133 with 512 segments).
 inline int scan_segments(long long units, int blocks, int wanted) {
   long long s = wanted / units;
-  if (s > blocks / 4) s = blocks / 4;
+  if (s > blocks) s = blocks;
+  while (s * s > 32ll * blocks) --s;
   return s < 1 ? 1 : (int)s;
 }
-// `first` of a forward call's segments, of which there are more than one
 hipError_t launch_scan_walk(const ScanWalk& A, bool bf16, hipStream_t stream);
 // The states of a forward walk A and, with the same sizes, of a walk back U, blocks of each
 hipError_t launch_scan_walks(const ScanWalk& A, const ScanWalk& U, bool bf16, hipStream_t stream);

@@ -9,6 +9,13 @@
 //   o_i = exp(l_i) S C_i + sum_j M_ij x_j
 //   S'  = exp(l_end) S + sum_j (exp(l_end - l_j) dtv_j x_j) B_j^T
 // all of them matrix products. l is summed in float64, so that the differences keep their digits.
+//
+// Float32 factors go into the matrix products as three bf16 pieces each, whose products are as exact as
+// float32's, at 3 (beside a bf16 factor) or 6 times a bf16 product's work. That work bounds prompts, not memory: at 131072 tokens, 8 heads of 128 x 128, 370 GFLOP,
+// 310 us at the rate of a large bf16 product and 190 us of memory traffic. Measured 552 us (this kernel 390-470,
+// the walk 150, gates 13, join 11); 8 x 4096 tokens, 16 heads of 128 x 64: 151 us (106, 38, 9, 7). A wave's vector
+// work (splitting, decays) takes as long as its matrix work and two waves per SIMD, all that registers and LDS
+// hold, do not overlap the two wholly.
 
 #include "sdm_device.hpp"
 #include "sdm_internal.hpp"
@@ -47,7 +54,9 @@ struct Tiles {
 
 // ------------------------------------------------------------------ prompts
 // One workgroup walks the blocks of a segment of a (sequence, head, 64 channels) unit with the state in
-// the accumulators of its matrix products: wave w holds channels 16 w .. 16 w + 15, all d_k.
+// the accumulators of its matrix products: wave w holds channels 16 w .. 16 w + 15, all d_k. So the state is
+// never stored between blocks, and each wave splits its own part of it only. Blocks of 64 tokens: the state's
+// products are shared by more tokens than in smaller ones, M grows with their square.
 template <bool BF16, int NK>
 __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, ScanWs W, ScanGates R) {
   using TL = Tiles<BF16, NK>;
@@ -392,7 +401,8 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanArgs A, ScanPlan L, Sc
 }
 
 // ------------------------------------------------------------------ single tokens
-// The state goes through the registers once, 16 bytes a lane; LR lanes hold a channel's row.
+// The state goes through the registers once, 16 bytes a lane; LR lanes hold a channel's row. Memory bounds it:
+// 64 sequences, 16 heads of 128 x 128 (135 MB) take 31 us, 4.3 TB/s.
 template <bool BF16, int LR>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs A) {
   constexpr int RW = 64 / LR;  // rows per wave

@@ -19,6 +19,10 @@
 // the end), then every block by itself. A workgroup of 8 waves takes one block of one group and some of its
 // heads, one after the other, and sums their dB and dC in registers; G is formed once. Every product runs on
 // the matrix cores with float32 factors as three bf16 pieces.
+//
+// 4 x 2048 tokens, 8 heads of 128 x 128: 151 us, of which the blocks take 93, the walks 42, their join 8, the
+// sums 6, gates 5. The blocks' matrix work takes 20% of their time and their vector work 45%: LDS (142 KB) holds
+// one workgroup per compute unit, whose 8 waves meet about ten times a head.
 
 #include "sdm_device.hpp"
 #include "sdm_internal.hpp"

@@ -11,7 +11,8 @@ namespace {
 
 // ------------------------------------------------------------------ time steps
 // A workgroup takes 64 tokens of a sequence, all heads: dt comes in along the heads, goes through LDS and
-// is summed along the tokens, one per lane.
+// is summed along the tokens, one per lane. 9 us for 8 x 4096 tokens of 16 heads (one wave per head instead of
+// four: 8 us there, but 15 instead of 13 at 131072 tokens of 8).
 template <int Q>
 __global__ void __launch_bounds__(256) scan_gates_kernel(ScanArgs A, ScanGates g) {
   __shared__ float tile[64][65];
@@ -48,7 +49,8 @@ __global__ void __launch_bounds__(256) scan_gates_kernel(ScanArgs A, ScanGates g
 // first is stored (backward: to the gradient of the state after it), and the decay up to there, by which the
 // state before the segment, which is known only behind this walk, still has to be multiplied. So one pass over
 // the tokens does: a pass for the segments' ends first took 33 us more (4 x 2048 tokens, 8 heads of 128 x 128).
-// A walk of one segment starts from the call's state and stores all.
+// A walk of one segment starts from the call's state and stores all. Both walks at that size: 42 us, of which
+// the 117 MB of states take 24; the forward pass's, without states, is bound like the kernel behind it.
 // TURN: results as [channel][d_k] tiles, whose lanes hold 4 consecutive channels, and turned states; else
 // the other way round. Each is stored the way the products that read it take it.
 constexpr int kPB = 64;

@@ -38,6 +38,9 @@ CASES = [
     (1100, 24, ("f32", "f32", "f32"), "f32", 2, "silu", True, True),
     (1026, 72, ("f32", "bf16", "f32"), "f32", 513, "silu", True, True),
     (600, 136, ("bf16", "bf16", "bf16"), "bf16", 200, "none", True, True),
+    (2000, 40, ("f32", "f32", "f32"), "f32", 1000, "silu", True, True),       # more groups than workgroups
+    (3000, 24, ("bf16", "f32", "bf16"), "bf16", 1000, "sigmoid", True, True),  # that begin and end anywhere in their rows
+    (2310, 1032, ("f32", "f32", "bf16"), "f32", 33, "silu", True, True),
 ]
 
 

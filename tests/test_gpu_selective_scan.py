@@ -92,6 +92,8 @@ CASES = [
     (1, 192, 1, 1, 72, 200, None, True, True),
     (2, 257, 2, 2, 96, 256, [300, -4], False, True),
     (3, 0, 2, 1, 16, 16, None, True, True),
+    (70, 200, 8, 2, 16, 16, None, True, True),          # as many units as fill the chip: one segment
+    (20, 300, 8, 1, 24, 16, [300, 150] * 10, True, True),  # segments of several blocks
 ]
 
 
@@ -207,6 +209,9 @@ GRAD = [
     (2, 129, 2, 2, 96, 256, [300, -4], False, True),
     (1, 70, 8, 1, 24, 40, None, True, True),
     (3, 0, 2, 1, 16, 16, None, True, True),
+    (40, 200, 8, 2, 16, 16, None, True, True),             # one segment of several blocks
+    (10, 300, 8, 1, 40, 72, [300, 150, 0, 63, 64] * 2, True, True),  # segments of several blocks
+    (64, 100, 8, 1, 24, 136, None, False, True),           # several heads and channel blocks a workgroup
 ]
 
 

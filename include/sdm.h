@@ -490,7 +490,8 @@ sdm_status sdm_selective_scan_step(const sdm_scan_shape* shape, const void* x, c
                                    float* state, float* o, void* stream);
 
 /* Bytes of device memory sdm_selective_scan_backward needs as workspace: the states and their
- * gradients at every 64th token, per-head sums, and partial gradients of Bm and Cm. 0 if the
+ * gradients at every 64th token (float32 inputs: 32nd; d_v up to a multiple of 64, d_k to 32, 64
+ * or 128) and between segments, per-head sums, and partial gradients of Bm and Cm. 0 if the
  * shape is invalid, or too large for the gradient: B * (T / 32 + 1) * H <= 2^22. */
 size_t sdm_selective_scan_backward_workspace_bytes(const sdm_scan_shape* shape);
 

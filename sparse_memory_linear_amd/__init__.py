@@ -362,13 +362,13 @@ def recurrent_chunked(shape: Shape, widx, wgt, ridx, rgt, v, alpha, beta, M, o, 
 
 # ----------------------------------------------------------------------------- convolution, scan, norm
 _torch = None  # torch, and the types of the tensors by the sdm_dtype: looked up once, on the first call
-_TYPES = ()
+_TYPES = {}
 
 
 def _load_torch():
     global _torch, _TYPES
     import torch
-    _TYPES = (torch.float32, torch.bfloat16, torch.int32)
+    _TYPES = dict(enumerate((torch.float32, torch.bfloat16, torch.int32)))
     _torch = torch
 
 
@@ -388,9 +388,8 @@ class _Args:
     def _take(self, name, t, dtype):
         if t is None:
             raise ValueError(f"{self.where}: {name} is missing")
-        want = _TYPES[dtype] if 0 <= dtype < len(_TYPES) else f"of sdm_dtype {dtype}"
-        if t.dtype is not want:
-            raise ValueError(f"{self.where}: {name} is {t.dtype}, not {want}")
+        if t.dtype is not _TYPES.get(dtype):
+            raise ValueError(f"{self.where}: {name} is {t.dtype}, not {_TYPES.get(dtype, f'of sdm_dtype {dtype}')}")
         d = t.get_device()
         if d != self.device or d < 0:
             if d < 0:
@@ -416,6 +415,8 @@ class _Args:
         """[B, T, width], or [B, T, ...] with the last dimensions flattened to `width`: rows `ld` apart."""
         p = self._take(name, t, dtype)
         shape, stride = t.shape, t.stride()
+        if shape == (B, T, width) and stride == (T * ld, ld, 1):
+            return p
         ok = len(shape) >= 3 and shape[0] == B and shape[1] == T
         inner = 1
         for d in range(len(shape) - 1, 1, -1):
@@ -438,17 +439,18 @@ class _Args:
 
     def call(self, shape, stream, *args):
         """Runs the entry point on `stream`, or on the current stream of the tensors' GPU."""
-        f, dev, cuda = getattr(lib(), self.where), self.device, _torch.cuda
+        f, dev, C = getattr(_lib or lib(), self.where), self.device, _torch._C
+        here = C._cuda_getDevice() if dev >= 0 else _torch.cuda.current_device()  # (tensors there: initialised)
         if dev < 0:
-            dev = cuda.current_device()
+            dev = here
         if stream is None:
-            stream = _torch._C._cuda_getCurrentRawStream(dev)
+            stream = C._cuda_getCurrentRawStream(dev)
         elif not isinstance(stream, int):
             stream = stream.cuda_stream
-        if dev == cuda.current_device():
+        if dev == here:
             code = f(ctypes.byref(shape), *args, stream)
         else:
-            with cuda.device(dev):
+            with _torch.cuda.device(dev):
                 code = f(ctypes.byref(shape), *args, stream)
         if code != 0:
             raise SdmError(code, self.where)

@@ -12,8 +12,8 @@
 //
 // Float32 factors go into the matrix products as three bf16 pieces each, whose products are as exact as
 // float32's, at 3 (beside a bf16 factor) or 6 times a bf16 product's work. That work bounds prompts, not memory: at 131072 tokens, 8 heads of 128 x 128, 370 GFLOP,
-// 310 us at the rate of a large bf16 product and 190 us of memory traffic. Measured 552 us (this kernel 390-470,
-// the walk 150, gates 13, join 11); 8 x 4096 tokens, 16 heads of 128 x 64: 151 us (106, 38, 9, 7). A wave's vector
+// 310 us at the rate of a large bf16 product and 190 us of memory traffic. Measured 542 us (this kernel 390-470,
+// the walk 150, gates 13, join 11); 8 x 4096 tokens, 16 heads of 128 x 64: 149 us (104, 38, 9, 7). A wave's vector
 // work (splitting, decays) takes as long as its matrix work and two waves per SIMD, all that registers and LDS
 // hold, do not overlap the two wholly.
 

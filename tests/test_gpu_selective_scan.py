@@ -278,3 +278,31 @@ def test_gradient_of_differences(sdm):
     got = sum((v.double() * w.double()).sum() for v, w in zip(dirs, (grad["dxbc"], grad["ddt"][..., :H], grad["dA_log"], grad["dD"])))
     most = sum(s.abs().sum() for s in slope)
     assert abs(sum(s.sum() for s in slope) - got) <= 2e-3 * most
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,H", [(1, 200, 2), (40, 130, 8), (2, 0, 2), (1, 20, 1)])
+def test_gradient_without_states(sdm, dtype, B, T, H):
+    """States that are left out are zeros; a first state's gradient that is not wanted changes nothing."""
+    c = Case(B, T, H, 1, 24, 40, dtype, state=True, seed=3)
+    c.s_in.zero_()
+    c.ds_out.zero_()
+    want = backward(sdm, c)
+    s_in, ds_out = c.s_in, c.ds_out
+    c.ds_out = None
+    got = backward(sdm, c)
+    for k, v in want.items():
+        assert torch.equal(got[k], v), k
+    c.s_in, c.ds_out = None, ds_out  # (and so no ds_in)
+    got = backward(sdm, c)
+    for k, v in want.items():
+        assert k == "ds_in" or torch.equal(got[k], v), k
+    # ds_in alone
+    c.ds_out = None
+    end = torch.full_like(s_in, 7.0)
+    o = {k: torch.full_like(v, 7.0) for k, v in want.items()}
+    sh = c.shape(sdm)
+    ws = torch.empty(sdm.selective_scan_backward_workspace_bytes(sh), dtype=torch.uint8, device="cuda")
+    sdm.selective_scan_backward(sh, *c.split(c.xbc), c.dt, c.A_log, c.dt_bias, c.go, *c.split(o["dxbc"]), o["ddt"][..., :H],
+                                o["dA_log"], o["ddt_bias"], ws, D=c.D, dD=o["dD"], ds_in=end)
+    assert torch.equal(end, want["ds_in"]) and torch.equal(o["dxbc"], want["dxbc"]) and torch.equal(o["ddt"], want["ddt"])

@@ -431,13 +431,26 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs A) {
   if (live && k == 0) A.o[(long long)bh * A.P + p] = fmaf(A.D ? A.D[h] : 0.f, x, o);
 }
 
+// What a call split into s segments takes, in us at d_k 128: a block of this kernel takes 4 where a workgroup has
+// its compute unit for itself and 6.5 where two share it, a block of the walk 2.4; walk and join start in 9 and
+// move four states per segment. So 8 x 4096 tokens of 16 heads (128 units of 64 channels) run in 4 segments (145
+// us; 246 in one), but 16 x 2000 tokens in one (133; 143 in two), and 16 x 100 too (20; 41 in two).
+double split_cost(const sdm_scan_shape& S, long long units, int blocks, int s) {
+  const int run = (blocks + s - 1) / s;
+  const double block = units * s <= 256 ? 4.0 : 6.5 * (double)((units * s + 511) / 512);
+  if (s == 1) return run * block;
+  return run * (block + 2.4) + 9.0 + s / 8.0 + (double)s * S.B * S.H * S.d_v * S.d_k * 16.0 / 4.5e6;
+}
+
 ScanPlan plan_of(const sdm_scan_shape& S) {
   const int Q = S.in_dtype == SDM_BF16 ? block_tokens<true>() : block_tokens<false>();
   ScanPlan L;
   L.pblocks = (S.d_v + kPB - 1) / kPB;
   L.blocks = (S.T + Q - 1) / Q;
   const long long units = (long long)S.B * S.H * L.pblocks;
-  L.segments = scan_segments(units, L.blocks, 512);  // two workgroups per compute unit
+  L.segments = 1;
+  for (int s = scan_segments(units, L.blocks, 512); s > 1; s /= 2)  // up to two workgroups per compute unit
+    if (split_cost(S, units, L.blocks, s) < split_cost(S, units, L.blocks, L.segments)) L.segments = s;
   return L;
 }
 

@@ -20,8 +20,6 @@ namespace {
 
 constexpr int kRun = 16;      // tokens per thread
 constexpr int kStep = 4;      // tokens at a time
-constexpr int kBwdLanes = 64; // backward: threads along the channels, 4 channels each
-constexpr int kBwdRuns = 4;   // backward: token runs per workgroup
 
 // W consecutive channels of a row as they lie in memory
 template <bool BF16, int W>
@@ -141,15 +139,17 @@ __global__ void __launch_bounds__(256) conv_kernel(ConvArgs A, int quads, long l
 }
 
 // ------------------------------------------------------------------ backward
-// A workgroup takes 256 channels and 4 consecutive runs of one sequence; its sums of dw and dbias over
-// those tokens go to one row of `part`, [workgroup][K+1][C].
-template <bool BF16, int K>
-__global__ void __launch_bounds__(kBwdLanes * kBwdRuns) conv_backward_kernel(ConvArgs A, int groups) {
-  __shared__ float red[kBwdRuns][kBwdLanes * 4];
-  const int lane = threadIdx.x % kBwdLanes, sub = threadIdx.x / kBwdLanes;
-  const int c0 = ((int)blockIdx.y * kBwdLanes + lane) * 4;
+// A workgroup takes LANES x 4 channels and RUNS consecutive runs of one sequence; its sums of dw and dbias over
+// those tokens go to one row of `part`, [workgroup][K+1][C]. 64 lanes, or 8 for up to 128 channels, which leave
+// most of 64 idle (64 x 2048 tokens of 64 channels: 27 us, 53 with 64 lanes).
+template <bool BF16, int K, int LANES>
+__global__ void __launch_bounds__(256) conv_backward_kernel(ConvArgs A, int groups) {
+  constexpr int RUNS = 256 / LANES;
+  __shared__ float red[RUNS][LANES * 4];
+  const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+  const int c0 = ((int)blockIdx.y * LANES + lane) * 4;
   const int b = (int)(blockIdx.x / groups), group = (int)(blockIdx.x % groups);
-  const int t0 = (group * kBwdRuns + sub) * kRun;
+  const int t0 = (group * RUNS + sub) * kRun;
   const int n = sequence_length(A.lengths, b, A.T);
   const bool live = c0 < A.C;
   float dw[K][4] = {}, db[4] = {};
@@ -252,44 +252,55 @@ __global__ void __launch_bounds__(kBwdLanes * kBwdRuns) conv_backward_kernel(Con
 #pragma unroll
     for (int e = 0; e < 4; ++e) red[sub][lane * 4 + e] = j < K ? dw[j < K ? j : 0][e] : db[e];
     __syncthreads();
-    const int c = threadIdx.x;
-    float s = 0.f;
+    const int c = threadIdx.x, ch = (int)blockIdx.y * LANES * 4 + c;
+    if (c < LANES * 4 && ch < A.C) {
+      double s = 0.0;
 #pragma unroll
-    for (int r = 0; r < kBwdRuns; ++r) s += red[r][c];
-    const int ch = (int)blockIdx.y * kBwdLanes * 4 + c;
-    if (ch < A.C) A.part[((long long)blockIdx.x * (K + 1) + j) * A.C + ch] = s;
+      for (int r = 0; r < RUNS; ++r) s += (double)red[r][c];
+      A.part[((long long)blockIdx.x * (K + 1) + j) * A.C + ch] = (float)s;
+    }
   }
 }
-static_assert(kBwdRuns == 4, "the reduction gives each thread one channel");
 
-// dw[c][j] and dbias[c] from the workgroups' sums, added in their order in float64: 64 columns x 4 row lanes
-// per workgroup, eight loads of each in flight
-__global__ void __launch_bounds__(256) conv_sum_kernel(const float* part, float* dw, float* dbias, int C, int K,
-                                                       long long n) {
-  __shared__ double red[4][64];
-  const int lane = threadIdx.x & 63, r = threadIdx.x >> 6;
-  const int col = (int)blockIdx.x * 64 + lane, cols = (K + 1) * C;
+// dw[c][j] and dbias[c] from the workgroups' sums, added in their order in float64: COLS columns x 1024 / COLS
+// row lanes per workgroup, eight loads of each in flight. 8 columns where there are many sums of few (540 rows
+// and more): of 8192 rows of 24 columns 64 took 50 us more.
+template <int COLS>
+__global__ void __launch_bounds__(1024) conv_sum_kernel(const float* part, float* dw, float* dbias, int C, int K,
+                                                        long long n) {
+  constexpr int ROWS = 1024 / COLS;
+  __shared__ double red[ROWS][COLS];
+  const int lane = threadIdx.x % COLS, r = threadIdx.x / COLS;
+  const int col = (int)blockIdx.x * COLS + lane, cols = (K + 1) * C;
   double s = 0.0;
   if (col < cols)
-    for (long long i = r; i < n; i += 32) {
+    for (long long i = r; i < n; i += 8 * ROWS) {
       float v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = part[min(i + 4 * u, n - 1) * cols + col];
+      for (int u = 0; u < 8; ++u) v[u] = part[min(i + ROWS * u, n - 1) * cols + col];
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (i + 4 * u < n) s += (double)v[u];
+        if (i + ROWS * u < n) s += (double)v[u];
     }
   red[r][lane] = s;
   __syncthreads();
+  for (int m = ROWS / 2; m >= 1; m >>= 1) {
+    if (r < m) red[r][lane] += red[r + m][lane];
+    __syncthreads();
+  }
   if (r == 0 && col < cols) {
-    const float v = (float)(((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane]);
+    const float v = (float)red[0][lane];
     const int j = col / C, c = col % C;
     if (j < K) dw[(long long)c * K + j] = v;
     else if (dbias) dbias[c] = v;
   }
 }
 
-int conv_bwd_groups(int T) { return T > 0 ? (T + kRun * kBwdRuns - 1) / (kRun * kBwdRuns) : 1; }
+int conv_bwd_lanes(int C) { return C <= 128 ? 8 : 64; }
+int conv_bwd_groups(int T, int C) {
+  const int tokens = kRun * (256 / conv_bwd_lanes(C));
+  return T > 0 ? (T + tokens - 1) / tokens : 1;
+}
 
 template <bool BF16>
 hipError_t launch_conv_k(const ConvArgs& A, hipStream_t stream) {
@@ -308,13 +319,16 @@ hipError_t launch_conv_k(const ConvArgs& A, hipStream_t stream) {
 
 template <bool BF16>
 hipError_t launch_conv_backward_k(const ConvArgs& A, hipStream_t stream) {
-  const int groups = conv_bwd_groups(A.T);
+  const int groups = conv_bwd_groups(A.T, A.C), lanes = conv_bwd_lanes(A.C);
   const long long blocks = (long long)A.B * groups;
-  const dim3 grid((unsigned)blocks, (unsigned)((A.C + kBwdLanes * 4 - 1) / (kBwdLanes * 4)));
+  const dim3 grid((unsigned)blocks, (unsigned)((A.C + lanes * 4 - 1) / (lanes * 4)));
   switch (A.K) {
-#define SDM_CONV(KK)                                                                                              \
-  case KK:                                                                                                        \
-    hipLaunchKernelGGL((conv_backward_kernel<BF16, KK>), grid, dim3(kBwdLanes * kBwdRuns), 0, stream, A, groups); \
+#define SDM_CONV(KK)                                                                                             \
+  case KK:                                                                                                       \
+    if (lanes == 8)                                                                                              \
+      hipLaunchKernelGGL((conv_backward_kernel<BF16, KK, 8>), grid, dim3(256), 0, stream, A, groups);            \
+    else                                                                                                         \
+      hipLaunchKernelGGL((conv_backward_kernel<BF16, KK, 64>), grid, dim3(256), 0, stream, A, groups);           \
     break;
     SDM_CONV(2) SDM_CONV(3) SDM_CONV(4) SDM_CONV(5) SDM_CONV(6) SDM_CONV(7) SDM_CONV(8)
 #undef SDM_CONV
@@ -323,15 +337,19 @@ hipError_t launch_conv_backward_k(const ConvArgs& A, hipStream_t stream) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int cols = (A.K + 1) * A.C;
-  hipLaunchKernelGGL(conv_sum_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, stream, A.part, A.dw, A.dbias,
-                     A.C, A.K, blocks);
+  if (blocks > 512 && cols < 64 * 64)
+    hipLaunchKernelGGL(conv_sum_kernel<8>, dim3((unsigned)((cols + 7) / 8)), dim3(1024), 0, stream, A.part, A.dw,
+                       A.dbias, A.C, A.K, blocks);
+  else
+    hipLaunchKernelGGL(conv_sum_kernel<64>, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, stream, A.part, A.dw,
+                       A.dbias, A.C, A.K, blocks);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t conv_backward_workspace_bytes(int B, int T, int C, int K) {
-  return align_up((size_t)B * conv_bwd_groups(T) * (K + 1) * C * 4);
+  return align_up((size_t)B * conv_bwd_groups(T, C) * (K + 1) * C * 4);
 }
 
 hipError_t launch_conv(const ConvArgs& A, hipStream_t stream) {

@@ -95,6 +95,9 @@ def test_calls_continue_from_the_state(sdm, dtype, cuts):
     (4, 37, 264, 4, "silu", 16, True, True, True),
     (1, 300, 72, 3, "silu", 0, False, False, True),
     (2, 0, 16, 4, "silu", 0, False, True, True),
+    (3, 1200, 8, 2, "none", 8, False, True, True),     # several workgroups of few channels
+    (2, 1100, 128, 8, "silu", 0, True, True, True),
+    (9, 3900, 136, 3, "silu", 0, False, True, True),   # many rows of few sums
 ])
 def test_gradients(sdm, dtype, B, T, C, K, act, gap, ragged, bias, state):
     d = make(B, T, C, K, dtype, gap, bias, state, seed=T)

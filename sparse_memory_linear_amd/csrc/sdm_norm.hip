@@ -178,26 +178,30 @@ __global__ void __launch_bounds__(256) norm_narrow_kernel(NormArgs A, long long 
 
 // ------------------------------------------------------------------ backward
 // Workgroup k of `parts` takes rows [M k / parts, M (k+1) / parts) and keeps their column sums in
-// registers. WPR waves hold a row between them, NC octets a lane; a workgroup's row slots take its rows in
-// turn, so that with one wave a row no wave waits for another. part[k][4][D]: the gate sums of a group of
+// registers. WPR waves hold a row between them, or L lanes of one (196608 rows of 64: 62 us with 8, 263 with 64),
+// NC octets a lane; a workgroup's row slots take its rows in turn, so that with a wave or less a row no wave waits
+// for another. part[k][4][D]: the gate sums of a group of
 // rows that begins before workgroup k's rows and ends in them (0) or goes on behind them (1), dw_post (2)
 // and dw_pre (3); a group that lies in one workgroup's rows goes straight to dgate.
 __device__ __forceinline__ long long part_begin(long long M, int k, int parts) { return M * k / parts; }
 
-template <int NC, int WPR>
+template <int NC, int WPR, int L = 64>
 __global__ void __launch_bounds__(WPR > 4 ? 64 * WPR : 256, WPR > 8 ? 4 : NC * WPR > 4 ? 2 : 3) norm_backward_kernel(NormArgs A, long long per_gate, int parts) {
-  constexpr int WAVES = WPR > 4 ? WPR : 4, SLOTS = WAVES / WPR, LANES = 64 * WPR;
+  constexpr int WAVES = WPR > 4 ? WPR : 4, LANES = WPR > 1 ? 64 * WPR : L, SLOTS = 64 * WAVES / LANES;
   __shared__ float red[2][3][WAVES][2];  // by the row's parity: a row may have one meeting only
   int turn = 0;
   __shared__ __align__(16) float sums[SLOTS > 1 ? SLOTS * LANES * NC * 8 : 1];
-  const int octets = A.D / 8, wave = threadIdx.x >> 6, slot = wave / WPR, lane = threadIdx.x % LANES;
+  const int octets = A.D / 8, wave = threadIdx.x >> 6, slot = threadIdx.x / LANES, lane = threadIdx.x % LANES;
   const int k = blockIdx.x;
   const long long m0 = part_begin(A.M, k, parts), m1 = part_begin(A.M, k + 1, parts);
   const float inv = 1.f / (float)A.D;
   // sums of two values over a row, the same in all its lanes
   auto row_sum = [&](float& v, float& w, int which) {
-    v = wave_sum_f32(v);
-    w = wave_sum_f32(w);
+#pragma unroll
+    for (int k = (LANES < 64 ? LANES : 64) / 2; k >= 1; k >>= 1) {
+      v = add_xor_f32(v, k);
+      w = add_xor_f32(w, k);
+    }
     if (WPR > 1) {
       if ((threadIdx.x & 63) == 0) {
         red[turn][which][wave][0] = v;
@@ -246,14 +250,13 @@ __global__ void __launch_bounds__(WPR > 4 ? 64 * WPR : 256, WPR > 8 ? 4 : NC * W
   struct Octet {
     uint4 a, b;  // (bf16: a)
   } ry[NC], rr[NC], rt[NC], rd[NC];
-  auto fetch = [&](long long row) {  // (-1: none)
-    const int hi = __builtin_amdgcn_readfirstlane((int)(row >> 32)), lo = __builtin_amdgcn_readfirstlane((int)row);
-    const long long m = (long long)hi << 32 | (uint32_t)lo;  // (a wave's own)
+  auto fetch = [&](long long mm, long long row) {  // row mm + .. of the rows from mm (the same for all; -1: none)
+    const int below = (int)(row - mm);
     auto row_of = [&](const void* base, bool bf16, bool there) {
-      return block_rows((const char*)base + m * A.D * (bf16 ? 2 : 4), there && m >= 0 ? (uint32_t)A.D * (bf16 ? 2 : 4) : 0u);
+      return block_rows((const char*)base + mm * A.D * (bf16 ? 2 : 4), there && mm >= 0 ? (uint32_t)(SLOTS * A.D) * (bf16 ? 2 : 4) : 0u);
     };
     auto octet = [&](rsrc_t r, bool bf16, int o) {
-      const uint32_t at = o < octets ? (uint32_t)o * (bf16 ? 16 : 32) : kNowhere;
+      const uint32_t at = o < octets ? (uint32_t)(below * octets + o) * (bf16 ? 16 : 32) : kNowhere;
       return Octet{load16(r, at), load16(r, bf16 ? kNowhere : at + 16)};
     };
     const rsrc_t y = row_of(A.y, A.y_bf16, true), r = row_of(A.r, A.r_bf16, true), x = row_of(A.dx, false, A.w_pre != nullptr),
@@ -295,17 +298,17 @@ __global__ void __launch_bounds__(WPR > 4 ? 64 * WPR : 256, WPR > 8 ? 4 : NC * W
     return end < m1 ? end : m1;
   };
   auto row_at = [&](long long mm, long long g1) { return mm + slot < g1 ? mm + slot : g1 - 1; };
-  if (AHEAD && m0 < m1) fetch(row_at(m0, group_end(m0)));
+  if (AHEAD && m0 < m1) fetch(m0, row_at(m0, group_end(m0)));
   for (long long g0 = m0; g0 < m1;) {
     const long long grp = g0 / per_gate, end = summed ? (grp + 1) * per_gate : m1, g1 = group_end(g0);
     for (long long mm = g0; mm < g1; mm += SLOTS) {
       const bool live = mm + slot < g1;
       const long long m = row_at(mm, g1);  // (behind the last: that again, for nothing)
-      const long long gate_row = m / per_gate * A.D;
+      const long long gate_row = (summed ? grp : m) * A.D;  // (without sums: a gate of each token)
       turn ^= 1;
       float yn[NC][8], h[NC][8], t[NC][8], dr[NC][8];
       float ss = 0.f, none = 0.f;
-      if (!AHEAD) fetch(m);
+      if (!AHEAD) fetch(mm, m);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int o = lane + i * LANES;
@@ -318,7 +321,10 @@ __global__ void __launch_bounds__(WPR > 4 ? 64 * WPR : 256, WPR > 8 ? 4 : NC * W
           for (int e = 0; e < 8; ++e) ss = fmaf(yn[i][e], yn[i][e], ss);
         }
       }
-      if (AHEAD) fetch(mm + SLOTS < g1 ? row_at(mm + SLOTS, g1) : g1 < m1 ? row_at(g1, group_end(g1)) : -1);
+      if (AHEAD) {
+        const long long next = mm + SLOTS < g1 ? mm + SLOTS : g1 < m1 ? g1 : -1;
+        fetch(next, next < 0 ? next : row_at(next, next < g1 ? g1 : group_end(next)));
+      }
       float p = 1.f;
       if (A.w_post) {
         row_sum(ss, none, 0);
@@ -516,13 +522,19 @@ hipError_t launch_norm_backward(const NormArgs& A, hipStream_t stream) {
 #define SDM_NORM(NC, WPR)                                                                                            \
   hipLaunchKernelGGL((norm_backward_kernel<NC, WPR>), dim3((unsigned)parts), dim3(WPR > 4 ? 64 * WPR : 256), 0, stream, \
                      A, per, parts)
-  if (octets <= 64) SDM_NORM(1, 1);
+#define SDM_NORM_NARROW(L)                                                                                           \
+  hipLaunchKernelGGL((norm_backward_kernel<1, 1, L>), dim3((unsigned)parts), dim3(256), 0, stream, A, per, parts)
+  if (octets <= 8) SDM_NORM_NARROW(8);
+  else if (octets <= 16) SDM_NORM_NARROW(16);
+  else if (octets <= 32) SDM_NORM_NARROW(32);
+  else if (octets <= 64) SDM_NORM(1, 1);
   else if (octets <= 128) SDM_NORM(1, 2);
   else if (octets <= 256) SDM_NORM(1, 4);
   else if (octets <= 512) SDM_NORM(1, 8);
   else if (octets <= 1024) SDM_NORM(2, 8);
   else SDM_NORM(2, 16);
 #undef SDM_NORM
+#undef SDM_NORM_NARROW
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (A.M == 0 && A.gate) {

@@ -41,6 +41,9 @@ CASES = [
     (2000, 40, ("f32", "f32", "f32"), "f32", 1000, "silu", True, True),       # more groups than workgroups
     (3000, 24, ("bf16", "f32", "bf16"), "bf16", 1000, "sigmoid", True, True),  # that begin and end anywhere in their rows
     (2310, 1032, ("f32", "f32", "bf16"), "f32", 33, "silu", True, True),
+    (5000, 64, ("f32", "f32", "f32"), "f32", 8, "silu", True, True),           # several rows a wave
+    (901, 128, ("bf16", "f32", "f32"), "bf16", 901, "sigmoid", True, True),
+    (2049, 256, ("f32", "bf16", "bf16"), "f32", 0, "none", True, True),
 ]
 
 
